@@ -172,14 +172,16 @@ MLA_API mla_status_t mla_get_error(const void* plan, uint32_t* error_bits, mla_s
  *
  * parts with lse_i = -inf (no visible token in that shard) weigh nothing;
  * a row empty in every part gets out = 0, lse = -inf.
- *   part_out  bf16 [parts, rows, 512] (each part's mla_decode output, rows = B * Sq * H)
+ * Width D = d_latent: 512 for mla_decode outputs, 128 for the per-head outputs
+ * of mlap_attention over parts of a context (mla_prefill.h).
+ *   part_out  bf16 [parts, rows, D] (each part's output, rows = B * Sq * H)
  *   part_lse  fp32 [parts, rows]
- *   out       bf16 [rows, 512]     lse  fp32 [rows]
+ *   out       bf16 [rows, D]       lse  fp32 [rows]
  * part_out and out 16-byte aligned. One kernel, asynchronous on `stream`,
  * no allocation. */
 typedef struct {
   int32_t parts;    /* N >= 1 */
-  int32_t d_latent; /* must be 512 */
+  int32_t d_latent; /* 512 or 128 */
   int64_t rows;     /* rows per part, >= 0 */
 } mla_merge_desc_t;
 

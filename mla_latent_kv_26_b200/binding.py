@@ -1,4 +1,4 @@
-"""ctypes binding of ``libmla.so`` (include/mla.h): the same names, argument
+"""ctypes binding of ``libmla.so`` (include/mla.h, include/mla_prefill.h): the same names, argument
 marshalling only. Every step of the decode runs in the library's CUDA
 kernels; there is no fallback. Importing this module without the built
 library raises ``RuntimeError``.
@@ -33,6 +33,11 @@ EXPORTED = (
     "mla_combine", "mla_get_error", "mla_status_string", "mla_decode_noalloc", "mla_cache_insert",
     "mla_absorb_query", "mla_unabsorb_output", "mla_index_scores", "mla_topk", "mla_merge", "mla_decode_fp8",
     "mla_cache_insert_fp8",
+)
+
+# include/mla_prefill.h
+EXPORTED_PREFILL = (
+    "mlap_cache_read", "mlap_cache_read_fp8", "mlap_expand_kv", "mlap_attention_workspace_bytes", "mlap_attention",
 )
 
 DEFAULT_SOFTMAX_SCALE = 1.0 / math.sqrt(192.0)
@@ -137,6 +142,62 @@ def make_merge_desc(*, parts: int, rows: int, d_latent: int = 512) -> mla_merge_
     return mla_merge_desc_t(parts, d_latent, rows)
 
 
+class mlap_read_desc_t(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int32),
+        ("max_pages_per_seq", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32),
+        ("num_rows", ctypes.c_int32),
+        ("d_latent", ctypes.c_int32),
+        ("d_rope", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+    ]
+
+
+def make_read_desc(*, batch: int, max_pages_per_seq: int, num_pages: int, num_rows: int, d_latent: int = 512,
+                   d_rope: int = 64, page_size: int = 64) -> mlap_read_desc_t:
+    return mlap_read_desc_t(batch, max_pages_per_seq, num_pages, num_rows, d_latent, d_rope, page_size)
+
+
+class mlap_expand_desc_t(ctypes.Structure):
+    _fields_ = [
+        ("num_rows", ctypes.c_int32),
+        ("num_heads", ctypes.c_int32),
+        ("row_stride", ctypes.c_int32),
+        ("d_nope", ctypes.c_int32),
+        ("d_latent", ctypes.c_int32),
+        ("d_v", ctypes.c_int32),
+    ]
+
+
+def make_expand_desc(*, num_rows: int, num_heads: int, row_stride: int = 576, d_nope: int = 128, d_latent: int = 512,
+                     d_v: int = 128) -> mlap_expand_desc_t:
+    return mlap_expand_desc_t(num_rows, num_heads, row_stride, d_nope, d_latent, d_v)
+
+
+class mlap_attention_desc_t(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int32),
+        ("num_heads", ctypes.c_int32),
+        ("num_q", ctypes.c_int32),
+        ("num_k", ctypes.c_int32),
+        ("pe_stride", ctypes.c_int32),
+        ("causal", ctypes.c_int32),
+        ("softmax_scale", ctypes.c_float),
+        ("num_sms", ctypes.c_int32),
+        ("d_nope", ctypes.c_int32),
+        ("d_rope", ctypes.c_int32),
+        ("d_v", ctypes.c_int32),
+    ]
+
+
+def make_attention_desc(*, batch: int, num_heads: int, num_q: int, num_k: int, pe_stride: int = 576,
+                        causal: bool = True, softmax_scale: float = DEFAULT_SOFTMAX_SCALE, num_sms: int = 0,
+                        d_nope: int = 128, d_rope: int = 64, d_v: int = 128) -> mlap_attention_desc_t:
+    return mlap_attention_desc_t(batch, num_heads, num_q, num_k, pe_stride, int(bool(causal)), softmax_scale, num_sms,
+                                 d_nope, d_rope, d_v)
+
+
 def load_library(path: str) -> ctypes.CDLL:
     """A handle on a build of the library at ``path`` with every C signature set."""
     if not os.path.exists(path):
@@ -165,6 +226,14 @@ def load_library(path: str) -> ctypes.CDLL:
         "mla_decode_fp8": (ctypes.c_int, [D, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]),
         "mla_cache_insert_fp8": (ctypes.c_int, [ctypes.POINTER(mla_insert_desc_t), P, P, P, P, P, P, P, P, P, P]),
     }
+    RD, ED, AD = (ctypes.POINTER(t) for t in (mlap_read_desc_t, mlap_expand_desc_t, mlap_attention_desc_t))
+    sig.update({
+        "mlap_cache_read": (ctypes.c_int, [RD, P, P, P, P, P, P, P]),
+        "mlap_cache_read_fp8": (ctypes.c_int, [RD, P, P, P, P, P, P, P]),
+        "mlap_expand_kv": (ctypes.c_int, [ED, P, P, P, P, P, P]),
+        "mlap_attention_workspace_bytes": (ctypes.c_size_t, [AD]),
+        "mlap_attention": (ctypes.c_int, [AD, P, P, P, P, P, P, P, P, ctypes.c_size_t, P, P]),
+    })
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
         fn.restype = res
@@ -284,9 +353,40 @@ def mla_topk(desc, scores, valid_lens, indices, stream=None) -> int:
 
 
 def mla_merge(desc, part_out, part_lse, out, lse, stream=None) -> int:
-    """LSE merge of per-shard decode results [parts, rows, 512] / [parts, rows]."""
+    """LSE merge of per-part results [parts, rows, 512 or 128] / [parts, rows]."""
     return int(_lib.mla_merge(ctypes.byref(desc), _ptr(part_out), _ptr(part_lse), _ptr(out), _ptr(lse),
                               _stream(stream)))
+
+
+def mlap_cache_read(desc, kv_cache, block_table, row_offsets, starts, rows, error_word=None, stream=None) -> int:
+    """Rows of ragged runs of positions, read back from the paged bf16 cache."""
+    return int(_lib.mlap_cache_read(ctypes.byref(desc), _ptr(kv_cache), _ptr(block_table), _ptr(row_offsets),
+                                    _ptr(starts), _ptr(rows), _ptr(error_word), _stream(stream)))
+
+
+def mlap_cache_read_fp8(desc, kv_cache_fp8, block_table, row_offsets, starts, rows, error_word=None,
+                        stream=None) -> int:
+    """mlap_cache_read from the fp8 cache format."""
+    return int(_lib.mlap_cache_read_fp8(ctypes.byref(desc), _ptr(kv_cache_fp8), _ptr(block_table), _ptr(row_offsets),
+                                        _ptr(starts), _ptr(rows), _ptr(error_word), _stream(stream)))
+
+
+def mlap_expand_kv(desc, rows, wkv_b, row_count, kv, error_word=None, stream=None) -> int:
+    """Per-head keys and values [num_rows, H, 256] of cached rows."""
+    return int(_lib.mlap_expand_kv(ctypes.byref(desc), _ptr(rows), _ptr(wkv_b), _ptr(row_count), _ptr(kv),
+                                   _ptr(error_word), _stream(stream)))
+
+
+def mlap_attention_workspace_bytes(desc: mlap_attention_desc_t) -> int:
+    return int(_lib.mlap_attention_workspace_bytes(ctypes.byref(desc)))
+
+
+def mlap_attention(desc, q, kv, k_pe, cu_q, cu_k, out, lse, workspace, workspace_bytes: int, error_word=None,
+                   stream=None) -> int:
+    """Ragged attention of new tokens over expanded keys and values."""
+    return int(_lib.mlap_attention(ctypes.byref(desc), _ptr(q), _ptr(kv), _ptr(k_pe), _ptr(cu_q), _ptr(cu_k),
+                                   _ptr(out), _ptr(lse), _ptr(workspace), int(workspace_bytes), _ptr(error_word),
+                                   _stream(stream)))
 
 
 def mla_get_error(plan, stream=None):

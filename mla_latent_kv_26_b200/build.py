@@ -2,7 +2,7 @@
 
 Usage: ``python -m mla_latent_kv_26_b200.build [--force] [--verbose]``.
 The library links the CUDA runtime statically and exports only the C ABI of
-``include/mla.h``.
+``include/mla.h`` and ``include/mla_prefill.h``.
 """
 
 from __future__ import annotations
@@ -18,8 +18,9 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libmla.so")
 SOURCES = ["mla_api.cu", "mla_decode.cu", "mla_plan_combine.cu", "mla_insert.cu", "mla_absorb.cu",
-           "mla_indexer.cu"]
-HEADERS = ["common.cuh", "sm100.cuh"]
+           "mla_indexer.cu", "mla_cache_read.cu", "mla_expand_kv.cu", "mla_prefill_attention.cu"]
+HEADERS = ["common.cuh", "sm100.cuh", "prefill.cuh"]
+PUBLIC_HEADERS = ["mla.h", "mla_prefill.h"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -32,7 +33,7 @@ def nvcc_path() -> str:
 
 def _inputs():
     files = [os.path.join(CSRC, f) for f in SOURCES + HEADERS]
-    files.append(os.path.join(INCLUDE, "mla.h"))
+    files += [os.path.join(INCLUDE, f) for f in PUBLIC_HEADERS]
     files.append(os.path.abspath(__file__))
     return files
 

@@ -13,7 +13,7 @@ namespace mla {
 
 cudaError_t launch_plan(const PlanArgs& args, cudaStream_t stream);
 cudaError_t launch_combine(const CombineArgs& args, int tasks, cudaStream_t stream);
-cudaError_t launch_merge(const MergeArgs& args, cudaStream_t stream);
+cudaError_t launch_merge(const MergeArgs& args, int width, cudaStream_t stream);
 const void* decode_kernel_ptr(bool fp8);
 int decode_smem_bytes(bool fp8);
 int decode_threads(bool fp8);
@@ -318,7 +318,7 @@ mla_status_t mla_merge(const mla_merge_desc_t* desc, const void* part_out, const
                        mla_stream_t stream) {
   if (!desc) return MLA_ERR_INVALID_ARG;
   if (desc->parts < 1 || desc->rows < 0) return MLA_ERR_INVALID_ARG;
-  if (desc->d_latent != kDLatent) return MLA_ERR_UNSUPPORTED;
+  if (desc->d_latent != kDLatent && desc->d_latent != 128) return MLA_ERR_UNSUPPORTED;
   if (desc->rows == 0) return MLA_OK;
   if ((desc->rows + 7) / 8 > 0x7fffffffLL || desc->rows * desc->parts > (1LL << 40)) return MLA_ERR_UNSUPPORTED;
   if (!part_out || !part_lse || !out || !lse) return MLA_ERR_INVALID_ARG;
@@ -331,7 +331,7 @@ mla_status_t mla_merge(const mla_merge_desc_t* desc, const void* part_out, const
   a.lse = lse;
   a.parts = desc->parts;
   a.rows = desc->rows;
-  return launch_merge(a, (cudaStream_t)stream) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+  return launch_merge(a, desc->d_latent, (cudaStream_t)stream) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
 const char* mla_status_string(mla_status_t s) {

@@ -156,19 +156,23 @@ __global__ void __launch_bounds__(256) mla_combine_kernel(CombineArgs a) {
 }
 
 // Merge of `parts` results of the same rows computed over disjoint token
-// sets (one per context-parallel shard): one warp per row, lane l holding
-// columns [8l, 8l + 8) and [256 + 8l, 256 + 8l + 8).
+// sets (one per context-parallel shard, or per part of a long context): lanes
+// of a warp hold 8 columns each, so that a 512-wide row takes a warp twice
+// and a 128-wide row half a warp once.
 // lse = M + ln sum_i exp(lse_i - M), out = sum_i exp(lse_i - lse) * out_i;
 // parts with lse_i = -inf weigh nothing; all empty: out = 0, lse = -inf.
+template <int kWidth>
 __global__ void __launch_bounds__(256) mla_merge_kernel(MergeArgs a) {
-  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
+  constexpr int kLanes = kWidth / 8 < 32 ? kWidth / 8 : 32;  // lanes of a row
+  constexpr int kChunks = kWidth / 8 / kLanes;
+  const long long row = ((long long)blockIdx.x * 256 + threadIdx.x) / kLanes;
+  const int lane = threadIdx.x % kLanes;
   if (row >= a.rows) return;
   float m = -INFINITY;
   for (int i = 0; i < a.parts; ++i) m = fmaxf(m, a.part_lse[(size_t)i * a.rows + row]);
-  float acc[16];
+  float acc[8 * kChunks];
 #pragma unroll
-  for (int j = 0; j < 16; ++j) acc[j] = 0.f;
+  for (int j = 0; j < 8 * kChunks; ++j) acc[j] = 0.f;
   float sum = 0.f;
   if (m != -INFINITY) {
     for (int i = 0; i < a.parts; ++i) {
@@ -176,9 +180,9 @@ __global__ void __launch_bounds__(256) mla_merge_kernel(MergeArgs a) {
       if (l == -INFINITY) continue;
       const float e = expf(l - m);
       sum += e;
-      const uint4* src = reinterpret_cast<const uint4*>(a.part_out + ((size_t)i * a.rows + row) * kDLatent);
+      const uint4* src = reinterpret_cast<const uint4*>(a.part_out + ((size_t)i * a.rows + row) * kWidth);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < kChunks; ++h) {
         const uint4 v = src[lane + 32 * h];
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -191,9 +195,9 @@ __global__ void __launch_bounds__(256) mla_merge_kernel(MergeArgs a) {
     }
   }
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
-  uint4* dst = reinterpret_cast<uint4*>(a.out + (size_t)row * kDLatent);
+  uint4* dst = reinterpret_cast<uint4*>(a.out + (size_t)row * kWidth);
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
+  for (int h = 0; h < kChunks; ++h) {
     uint32_t w[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -205,9 +209,11 @@ __global__ void __launch_bounds__(256) mla_merge_kernel(MergeArgs a) {
   if (lane == 0) a.lse[row] = sum > 0.f ? m + logf(sum) : -INFINITY;
 }
 
-cudaError_t launch_merge(const MergeArgs& args, cudaStream_t stream) {
-  const long long blocks = (args.rows + 7) / 8;
-  mla_merge_kernel<<<(unsigned)blocks, 256, 0, stream>>>(args);
+cudaError_t launch_merge(const MergeArgs& args, int width, cudaStream_t stream) {
+  const int per_block = width == 128 ? 16 : 8;
+  const unsigned blocks = (unsigned)((args.rows + per_block - 1) / per_block);
+  if (width == 128) mla_merge_kernel<128><<<blocks, 256, 0, stream>>>(args);
+  else mla_merge_kernel<kDLatent><<<blocks, 256, 0, stream>>>(args);
   return cudaGetLastError();
 }
 

@@ -1,0 +1,63 @@
+// Definitions shared by the prefill kernels: bounded pipeline waits and the
+// error bits they report.
+#pragma once
+
+#include <stdint.h>
+
+#include "common.cuh"
+#include "sm100.cuh"
+
+namespace mla {
+namespace prefill {
+
+using namespace ptx;
+
+constexpr uint32_t kErrPosition = 0x10u;       // MLA_DEVERR_POSITION
+constexpr uint64_t kWaitNs = 2000000000ull;    // a pipeline wait gives up after 2 s: only a broken device gets there
+constexpr int kBox = 128 * 128;                // bytes of a 128-row x 64-column bf16 box (128-byte swizzle rows)
+
+MLA_DEV void set_error(uint32_t* word, uint32_t bits) {
+  if (word) atomicOr(word, bits);
+}
+
+// Bounded waits of one CTA: a wait that runs out raises the CTA's abort flag
+// and the caller's error word; every later wait then returns at once, except
+// the draining ones, which let copies and MMAs in flight finish.
+struct Waiter {
+  uint32_t* abort_flag;  // shared memory
+  uint32_t* err;         // device word or nullptr
+  MLA_DEV bool aborted() const { return *reinterpret_cast<volatile uint32_t*>(abort_flag) != 0; }
+  MLA_DEV void fail() {
+    *reinterpret_cast<volatile uint32_t*>(abort_flag) = 1u;
+    set_error(err, kErrTimeout);
+  }
+  MLA_DEV bool wait(uint64_t* bar, uint32_t parity, bool drain = false) {
+    const uint32_t a = smem_addr(bar);
+    if (mbar_try_wait(a, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    while (true) {
+      if (mbar_try_wait(a, parity)) return true;
+      if (!drain && aborted()) return false;
+      if (global_timer_ns() - t0 > kWaitNs) {
+        fail();
+        return false;
+      }
+    }
+  }
+  // Every lane waits; the outcome is made warp-uniform so that no lane leaves
+  // a loop its warp-mates stay in.
+  MLA_DEV bool wait_warp(uint64_t* bar, uint32_t parity) { return __all_sync(~0u, wait(bar, parity)); }
+};
+
+// Range [*first, *first + return) of sequence b in ragged rows [0, rows):
+// offsets outside [0, rows] or out of order are clipped into it, so that no
+// caller's offsets make an access leave the rows.
+MLA_DEV int ragged_range(const int32_t* offsets, int b, int rows, int* first) {
+  const int o0 = __ldg(offsets + b), o1 = __ldg(offsets + b + 1);
+  const int a0 = min(max(o0, 0), rows);
+  *first = a0;
+  return min(max(o1, a0), rows) - a0;
+}
+
+}  // namespace prefill
+}  // namespace mla

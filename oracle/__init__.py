@@ -34,6 +34,8 @@ Modules:
 * :mod:`oracle.indexer` — the sparse-attention indexer ("DeepSeek-V3.2-Exp
   unboxing", the Indexer section): fp8 index scores per (query, key) and the
   top-k positions that the sparse decode attends to.
+* :mod:`oracle.prefill` — prefill of a chunk of new tokens: the cached rows read
+  back, their per-head keys and values, ragged (causal) attention over them.
 
 Pins (tests/test_oracle.py): absorption equivalence against the unabsorbed
 path, single-key exactness, probabilities summing to one, brute force with
@@ -65,3 +67,4 @@ from .cache_insert import rms_norm, rope_pairs, cache_insert  # noqa: F401,E402
 from .fp8_cache import (e4m3_round, quantize_rows, dequantize_rows, fp8_roundtrip_cache, unpack_rows,  # noqa: F401,E402
                         dequantize_cache)
 from .indexer import index_scores, topk_positions  # noqa: F401,E402
+from . import prefill  # noqa: F401,E402
