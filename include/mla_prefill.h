@@ -126,7 +126,7 @@ MLA_API mla_status_t mlap_expand_kv(const mlap_expand_desc_t* desc, const void* 
  *   out    bf16 [num_q, H, 128]   lse  fp32 [num_q, H] (natural log)
  *   workspace   at least mlap_attention_workspace_bytes: partial results of split
  *          work; calls that may overlap on the GPU need one each
- * q, kv, k_pe, out, workspace 16-byte aligned. cu_q / cu_k beyond num_q / num_k or
+ * q, kv, k_pe 16-byte aligned, out and workspace 32-byte aligned. cu_q / cu_k beyond num_q / num_k or
  * out of order set MLA_DEVERR_SEQ_LEN and are clipped. Two kernels. Probabilities
  * are rounded to bf16 for the product with the values (their sums are not);
  * everything else is float32. The result does not depend on timing: work is

@@ -9,25 +9,35 @@
 //
 // Work. An item is (sequence, block of 256 queries, head); its units are its
 // visible 128-key tiles. All units are laid end to end (sequence, block, head,
-// tile) and cut into one equal run per SM, so that every SM gets the same work
-// whatever the lengths. With blocks before heads, SMs that work on different
-// blocks of one sequence reach the same head, and so the same keys, at about
-// the same time and share them in L2. An item cut by a run boundary leaves
-// float32 partials with their own lse, merged by the second kernel.
+// tile) and cut into one equal run per CTA pair, so that every SM gets the same
+// work whatever the lengths. With blocks before heads, pairs that work on
+// different blocks of one sequence reach the same head, and so the same keys,
+// at about the same time and share them in L2. An item cut by a run boundary
+// leaves float32 partials with their own lse, merged by the second kernel.
 //
-// Per CTA (320 threads), two query tiles of 128 rows share each key tile:
-//   warps 0-3, 4-7  softmax of query tile 0 / 1, one thread per row: S from
-//                   TMEM, mask, maximum, exponentials, P (bf16) back over S in
-//                   TMEM; rescales O when the maximum grew by more than 2^8;
-//                   writes the finished rows
-//   warp 8          tcgen05 issuer: S_t = Q_t K^T (M 128, N 128, K 192, both from
-//                   shared memory), O_t += P_t V (P from TMEM, V read MN-major)
-//   warp 9          producer: Q tiles and K / V boxes by TMA; a ring of eight
-//                   16 KB boxes (128 rows x 64 columns): a key tile is K (two
-//                   boxes), k_pe (one), V (two)
-// The issuer alternates P_0 V, S_0, P_1 V, S_1, so that one tile's softmax runs
-// under the other's products. TMEM: S_0 S_1 (128 columns each, P in the lower
-// 64), O_0 O_1 (128 each): all 512 columns.
+// A CTA pair (cta_group::2) works on a block: S = Q K^T and O += P V with M 256,
+// 128 rows in each CTA. Each CTA loads half of every key tile (64 keys of K,
+// 64 columns of V), so that a tile costs the pair's SMs 40 KB each and three
+// tiles fit beside two Q buffers. TMEM of a CTA: O (128 columns) and three S
+// buffers; P (bf16) overwrites the lower half of its S. The scores run up
+// to three tiles ahead of the values, S(i + 3) behind P(i) V(i), and the two
+// softmax warpgroups of a CTA take alternate tiles: neither the tensor cores nor
+// the exponentials wait for one another's latency. (One CTA with two query
+// tiles and one S buffer each has the tensor cores idle for the whole chain of
+// S, softmax, P V; it took 4400 cycles per 2560 of products.)
+//
+// Per CTA (384 threads):
+//   warps 0-3, 4-7  softmax of the even / odd key tiles, one thread per row: S
+//                   from TMEM, mask, maximum, exponentials, P; O is rescaled when
+//                   the row's maximum grew by more than 2^8 since its reference
+//                   (which the two warpgroups hand on tile by tile); each writes
+//                   half of the finished columns
+//   warps 8, 11     (even CTA) tcgen05 issuers, one thread each: scores; values.
+//                   The tensor core's queue is short, an issuer is held up while
+//                   its products run: with one issuer its own waits and address
+//                   arithmetic then left the tensor cores idle
+//   warp 9          producer by TMA: Q, V of tile i, K of tile i + 3
+//   warp 10         clears the value rows behind a sequence's end
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
@@ -43,15 +53,21 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 namespace prefill {
 
-constexpr int kAttnThreads = 320;
-constexpr int kTile = 128;                 // rows of a query tile, keys of a key tile
+constexpr int kAttnThreads = 384;
+constexpr int kTile = 128;                 // query rows of a CTA, keys of a key tile
 constexpr int kBlockQ = 2 * kTile;         // queries of an item
-constexpr int kRing = 8;
-constexpr int kQBoxes = 6;
-constexpr int kAttnSmem = 1024 + (kQBoxes + kRing) * kBox;
-constexpr uint32_t kTmemS = 0, kTmemO = 256, kTmemAll = 512;
+constexpr int kStages = 3;                 // key tiles in shared memory, and S buffers
+constexpr int kQBytes = 3 * kBox;          // 128 rows x 192
+constexpr int kHalfBox = kBox / 2;         // 64 rows x 64 columns
+constexpr int kKBytes = 3 * kHalfBox;      // 64 keys x 192 (two column blocks of K, k_pe)
+constexpr int kVBytes = kBox;              // 128 keys x 64
+constexpr int kStageBytes = kKBytes + kVBytes;
+constexpr int kAttnSmem = 1024 + 2 * kQBytes + kStages * kStageBytes;
+constexpr uint32_t kTmemO = 0, kTmemS = 128, kTmemAll = 512;
 constexpr float kGrowth = 8.0f;            // log2: O is rescaled when a row's maximum grew by more (p stays below 2^8)
-constexpr float kLn2 = 0.6931471805599453f;
+// Registers a thread after the split: the softmax warpgroups hold a row of
+// scores each. 256 * 200 + 128 * 104 = 64512 = the 384 * 168 launched.
+constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;
 
 // What the merge kernel needs about the item that run w starts and does not
 // finish: the number of runs it spans (0: none), its first query row, rows, head.
@@ -73,9 +89,11 @@ struct AttnArgs {
 };
 
 struct AttnMaps {
-  CUtensorMap q;   // [num_q, H * 192] boxes of 128 x 64
-  CUtensorMap kv;  // [num_k, H * 256]
-  CUtensorMap pe;  // [num_k, 64]
+  // [64 columns, rows, 64-column blocks] of bf16; boxes:
+  CUtensorMap q;   // 128 rows, 3 blocks (a head)
+  CUtensorMap k;   // 64 rows, 2 blocks
+  CUtensorMap v;   // 128 rows, 1 block
+  CUtensorMap pe;  // 64 rows, 1 block
 };
 
 MLA_DEV int ceil_tiles(int keys) { return (keys + kTile - 1) >> 7; }  // also for negative counts
@@ -195,16 +213,43 @@ MLA_DEV long long run_start(const AttnArgs& a, int w, Cursor* cur) {
   return quota;
 }
 
-struct AttnBars {
-  uint64_t full[kRing], empty[kRing];
-  uint64_t q_full, q_empty;
-  uint64_t s_full[2], p_full[2], o_full[2];
+struct AttnShared {
+  // key tile i uses entry i % 3; the even CTA's entries serve both CTAs
+  uint64_t k_full[kStages], v_full[kStages];   // even CTA: both CTAs' halves have landed
+  uint64_t p_full[kStages];                    // even CTA: the P of both CTAs' rows
+  uint64_t s_full[kStages], o_full[kStages];   // both: Q K(i)^T / P(i) V(i) done, so K(i) / V(i) may be overwritten
+  uint64_t q_full[2], q_empty[2];              // q_full: even CTA
+  uint64_t o_done;                             // both: an item's last P V is done
+  uint64_t o_empty;                            // even CTA: both CTAs have read an item's O
+  uint64_t v_landed[kStages];                  // V of a sequence's last tile, before its rows are cleared
+  uint64_t m_ready[4], fin[4];                 // per 32 rows: reference maximum of a tile, sums of an item
   uint64_t done;
   Cursor start;
   long long quota;
+  float m[2][kTile];                           // reference maximum after tile n, entry n % 2
+  float fin_m[2][2][kTile], fin_l[2][2][kTile];  // [item % 2][warpgroup]
   uint32_t tmem;
   uint32_t abort_flag;
 };
+
+// Entry and phase of a ring of kStages.
+struct RingPos {
+  int s = 0;
+  uint32_t phase = 0;
+  MLA_DEV void next() {
+    if (++s == kStages) {
+      s = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+// 32 bytes to global memory, 32-byte aligned.
+MLA_DEV void st_global_v8(void* dst, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
 
 MLA_DEV float max3(float a, float b, float c) {
   float d;
@@ -212,332 +257,407 @@ MLA_DEV float max3(float a, float b, float c) {
   return d;
 }
 
-__global__ void __launch_bounds__(kAttnThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     mla_prefill_attention_kernel(const __grid_constant__ AttnMaps maps, const AttnArgs a) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ AttnBars bars;
+  __shared__ AttnShared sh;
+  // both CTAs' layouts are the same: the pair's instructions use one set of offsets
   const uint32_t qbuf = (smem_addr(smem_raw) + 1023u) & ~1023u;
-  const uint32_t ring = qbuf + kQBoxes * kBox;
+  const uint32_t stages = qbuf + 2 * kQBytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  Waiter W{&bars.abort_flag, a.error};
+  const int rank = (int)cluster_ctarank(), worker = (int)cluster_id_x();
+  Waiter W{&sh.abort_flag, a.error};
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kRing; ++s) {
-      mbar_init(smem_addr(&bars.full[s]), 1);
-      mbar_init(smem_addr(&bars.empty[s]), 1);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(smem_addr(&sh.k_full[s]), 2);  // both producers, or both clearing warps
+      mbar_init(smem_addr(&sh.v_full[s]), 2);
+      mbar_init(smem_addr(&sh.p_full[s]), 8);  // four softmax warps of either CTA
+      mbar_init(smem_addr(&sh.s_full[s]), 1);
+      mbar_init(smem_addr(&sh.o_full[s]), 1);
+      mbar_init(smem_addr(&sh.v_landed[s]), 1);
     }
-    mbar_init(smem_addr(&bars.q_full), 1);
-    mbar_init(smem_addr(&bars.q_empty), 1);
-    for (int t = 0; t < 2; ++t) {
-      mbar_init(smem_addr(&bars.s_full[t]), 1);
-      mbar_init(smem_addr(&bars.p_full[t]), 4);  // the four softmax warps of the tile
-      mbar_init(smem_addr(&bars.o_full[t]), 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_addr(&sh.q_full[b]), 2);
+      mbar_init(smem_addr(&sh.q_empty[b]), 1);
     }
-    mbar_init(smem_addr(&bars.done), 1);
-    bars.abort_flag = 0u;
+    mbar_init(smem_addr(&sh.o_done), 1);
+    mbar_init(smem_addr(&sh.o_empty), 16);     // all softmax warps of both CTAs
+    for (int x = 0; x < 4; ++x) {
+      mbar_init(smem_addr(&sh.m_ready[x]), 1);
+      mbar_init(smem_addr(&sh.fin[x]), 2);     // the two softmax warps of the rows
+    }
+    mbar_init(smem_addr(&sh.done), 2);         // the two issuers
+    sh.abort_flag = 0u;
     fence_mbar_init();
-    a.info[blockIdx.x].pieces = 0;
+    if (rank == 0) a.info[worker].pieces = 0;
   }
   if (warp == 8) {
-    tmem_alloc(smem_addr(&bars.tmem), kTmemAll);
-    tmem_relinquish();
+    tmem_alloc_pair(smem_addr(&sh.tmem), kTmemAll);
+    tmem_relinquish_pair();
   }
   if (warp == 9) {
     Cursor c;
-    const long long quota = run_start(a, blockIdx.x, &c);
+    const long long quota = run_start(a, worker, &c);
     if (lane == 0) {
-      bars.start = c;
-      bars.quota = quota;
+      sh.start = c;
+      sh.quota = quota;
       prefetch_tmap(&maps.q);
-      prefetch_tmap(&maps.kv);
+      prefetch_tmap(&maps.k);
+      prefetch_tmap(&maps.v);
       prefetch_tmap(&maps.pe);
     }
   }
   tc_fence_before();
-  __syncthreads();
+  cluster_sync();
   tc_fence_after();
-  const uint32_t tmem = bars.tmem;
-  Cursor cur = bars.start;
+  const uint32_t tmem = sh.tmem;
+  Cursor cur = sh.start;
+  // an entry of the even CTA's barriers, for both CTAs
+  const auto leader = [&](uint64_t* bar) { return map_to_rank(smem_addr(bar), 0); };
+  const auto tail = [&](int j) { return cur.s.L < (j + 1) * kTile; };  // tile j reaches behind the sequence's end
 
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+  }
   if (warp == 9) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
-      int nb = 0, nq = 0;  // boxes and query blocks whose loads were issued
+      Cursor ahead = cur;  // position of Q and K, three tiles before V
+      RingPos pk, pv;
+      int nq = 0, jk = ahead.t0;
       bool ok = true;
+      const auto load_k = [&]() {
+        if (!ahead.more()) return true;
+        if (jk == ahead.t0) {
+          const int b = nq & 1;
+          if (!W.wait(&sh.q_empty[b], ((nq >> 1) & 1) ^ 1)) return false;
+          mbar_arrive_expect_tx_cluster(leader(&sh.q_full[b]), kQBytes);
+          tma_load_3d_pair(qbuf + b * kQBytes, &maps.q, 0, ahead.s.q0 + ahead.qb * kBlockQ + rank * kTile, 3 * ahead.h,
+                           leader(&sh.q_full[b]));
+          ++nq;
+        }
+        if (!W.wait(&sh.s_full[pk.s], pk.phase ^ 1)) return false;  // K of three tiles ago is done with
+        const uint32_t kf = leader(&sh.k_full[pk.s]), ks = stages + pk.s * kStageBytes;
+        const int row = ahead.s.k0 + jk * kTile + 64 * rank;
+        mbar_arrive_expect_tx_cluster(kf, kKBytes);
+        tma_load_3d_pair(ks, &maps.k, 0, row, 4 * ahead.h, kf);
+        tma_load_3d_pair(ks + 2 * kHalfBox, &maps.pe, 0, row, 0, kf);
+        pk.next();
+        if (++jk == ahead.t1()) {
+          ahead.next(a);
+          jk = ahead.t0;
+        }
+        return true;
+      };
+      for (int x = 0; x < kStages && ok; ++x) ok = load_k();
       for (; cur.more() && ok; cur.next(a)) {
-        const int rows = cur.s.n - cur.qb * kBlockQ;
-        if (!W.wait(&bars.q_empty, (nq & 1) ^ 1)) break;
-        const int boxes = rows > kTile ? 6 : 3;
-        mbar_arrive_expect_tx(smem_addr(&bars.q_full), boxes * kBox);
-        for (int x = 0; x < boxes; ++x)
-          tma_load_2d(qbuf + x * kBox, &maps.q, cur.h * 192 + 64 * (x % 3),
-                      cur.s.q0 + cur.qb * kBlockQ + kTile * (x / 3), smem_addr(&bars.q_full));
-        ++nq;
         const int t1 = cur.t1();
-        for (int j = cur.t0; j < t1 && ok; ++j) {
+        for (int j = cur.t0; j < t1; ++j, pv.next()) {
+          if (!(ok = W.wait(&sh.o_full[pv.s], pv.phase ^ 1))) break;  // V of three tiles ago is done with
+          const uint32_t vs = stages + pv.s * kStageBytes + kKBytes;
           const int row = cur.s.k0 + j * kTile;
-          for (int x = 0; x < 5; ++x) {  // K, K, k_pe, V, V
-            const int s = nb % kRing;
-            if (!(ok = W.wait(&bars.empty[s], ((nb / kRing) & 1) ^ 1))) break;
-            const uint32_t full = smem_addr(&bars.full[s]);
-            mbar_arrive_expect_tx(full, kBox);
-            if (x == 2) tma_load_2d(ring + s * kBox, &maps.pe, 0, row, full);
-            else tma_load_2d(ring + s * kBox, &maps.kv, cur.h * 256 + 64 * (x < 2 ? x : x - 1), row, full);
-            ++nb;
+          if (tail(j)) {
+            const uint32_t vl = smem_addr(&sh.v_landed[pv.s]);
+            mbar_arrive_expect_tx(vl, kVBytes);
+            tma_load_3d(vs, &maps.v, 0, row, 4 * cur.h + 2 + rank, vl);
+          } else {
+            const uint32_t vf = leader(&sh.v_full[pv.s]);
+            mbar_arrive_expect_tx_cluster(vf, kVBytes);
+            tma_load_3d_pair(vs, &maps.v, 0, row, 4 * cur.h + 2 + rank, vf);
           }
+          if (!(ok = load_k())) break;
         }
       }
-      // every issued copy lands before the CTA can exit
-      for (int i = max(0, nb - kRing); i < nb; ++i) W.wait(&bars.full[i % kRing], (i / kRing) & 1, true);
-      if (nq > 0) W.wait(&bars.q_full, (nq - 1) & 1, true);
+      // Every load was waited for by its reader, unless a wait ran out: then
+      // the copies in flight get ample time before the CTA exits.
+      if (W.aborted()) {
+        const uint64_t t = global_timer_ns();
+        while (global_timer_ns() - t < 10000000ull) {}
+      }
     }
     __syncwarp();
   } else if (warp == 8) {
-    // ------------------------------------------------------------ MMA issuer
-    // The whole warp walks the loop (it clears value rows together); lane 0 issues.
-    constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, 0, 0);
-    constexpr uint32_t idesc_o = idesc_bf16_f32(128, 128, 0, 1);
-    constexpr uint32_t idesc_half = idesc_bf16_f32(128, 64, 0, 1);
-    int nb = 0, nq = 0;        // boxes and query blocks consumed
-    int np[2] = {0, 0};        // P tiles consumed
-    bool ok = true;
-    const auto box = [&](int i) { return ring + (uint32_t)(i % kRing) * kBox; };
-    const auto wait_boxes = [&](int first, int count) {
-      bool good = true;
-      for (int i = first; i < first + count && good; ++i) good = W.wait_warp(&bars.full[i % kRing], (i / kRing) & 1);
-      return good;
-    };
-    const auto scores = [&](int t, int k) {  // S_t = Q_t K^T, K in boxes k .. k + 2
-      if (lane == 0) {
+    // ------------------------------------------------------------ MMA issuer: scores
+    if (rank == 0 && lane == 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(256, 128, 0, 0);
+      RingPos p;
+      int nq = 0;
+      bool ok = true;
+      for (; cur.more() && ok; cur.next(a), ++nq) {
+        const int t1 = cur.t1(), b = nq & 1;
+        if (!W.wait(&sh.q_full[b], (nq >> 1) & 1)) break;
+        const uint64_t qd = smem_desc_sw128(qbuf + b * kQBytes, 16, 1024);
+        for (int j = cur.t0; j < t1; ++j, p.next()) {
+          if (!(ok = W.wait(&sh.k_full[p.s], p.phase))) break;
+          if (!(ok = W.wait(&sh.o_full[p.s], p.phase ^ 1))) break;  // P V of three tiles ago has read this S entry
+          tc_fence_after();
+          // S = Q K^T; 16 columns are 32 bytes of a swizzled row
+          const uint64_t kd = smem_desc_sw128(stages + p.s * kStageBytes, 16, 1024);
+          const uint32_t st = tmem + kTmemS + 128 * p.s;
 #pragma unroll
-        for (int u = 0; u < 12; ++u)
-          mma_ss(tmem + kTmemS + 128 * t, smem_desc_sw128(qbuf + (3 * t + (u >> 2)) * kBox + (u & 3) * 32, 16, 1024),
-                 smem_desc_sw128(box(k + (u >> 2)) + (u & 3) * 32, 16, 1024), idesc_s, u > 0 ? 1u : 0u);
-        mma_commit(smem_addr(&bars.s_full[t]));
-      }
-    };
-    const auto release = [&](int first, int count) {
-      if (lane == 0)
-        for (int i = first; i < first + count; ++i) mma_commit(smem_addr(&bars.empty[i % kRing]));
-    };
-    for (; cur.more() && ok; cur.next(a)) {
-      const int t1 = cur.t1(), r0 = cur.qb * kBlockQ;
-      int e[2];
-      e[0] = min(t1, cur.s.tiles(r0 + kTile, a.causal));
-      e[1] = cur.s.n > r0 + kTile ? t1 : 0;
-      if (!(ok = W.wait_warp(&bars.q_full, nq & 1))) break;
-      ++nq;
-      if (!(ok = wait_boxes(nb, 3))) break;
-      tc_fence_after();
-      for (int t = 0; t < 2; ++t)
-        if (cur.t0 < e[t]) scores(t, nb);
-      release(nb, 3);
-      for (int j = cur.t0; j < t1 && ok; ++j) {
-        const int v = nb + 3, k_next = nb + 5;  // this tile's V boxes, the next tile's K boxes
-        bool v_ready = false, k_ready = false;
-        for (int t = 0; t < 2 && ok; ++t) {
-          if (j < e[t]) {
-            if (!v_ready) {
-              if (!(ok = wait_boxes(v, 2))) break;
-              const int valid = cur.s.L - j * kTile;
-              if (valid < kTile) {
-                // value rows behind the sequence's end: 0 * NaN is NaN, so they are cleared
-                for (int i = max(valid, 0) * 8 + lane; i < kTile * 8; i += 32) {
-                  st_shared_v4(box(v) + 16 * i, make_uint4(0, 0, 0, 0));
-                  st_shared_v4(box(v + 1) + 16 * i, make_uint4(0, 0, 0, 0));
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-              }
-              v_ready = true;
-            }
-            if (!(ok = W.wait_warp(&bars.p_full[t], np[t] & 1))) break;
-            ++np[t];
-            tc_fence_after();
-            if (lane == 0) {
-              const uint32_t o = tmem + kTmemO + 128 * t, p = tmem + kTmemS + 128 * t;
-              if (v % kRing != kRing - 1) {
-#pragma unroll
-                for (int u = 0; u < 8; ++u)
-                  mma_tmem_a(o, p + 8 * u, smem_desc_sw128(box(v) + 2048 * u, kBox, 1024), idesc_o,
-                             (j > cur.t0 || u > 0) ? 1u : 0u);
-              } else {  // the two boxes are the ring's last and first: one half at a time
-#pragma unroll
-                for (int u = 0; u < 8; ++u)
-#pragma unroll
-                  for (int x = 0; x < 2; ++x)
-                    mma_tmem_a(o + 64 * x, p + 8 * u, smem_desc_sw128(box(v + x) + 2048 * u, kBox, 1024), idesc_half,
-                               (j > cur.t0 || u > 0) ? 1u : 0u);
-              }
-              mma_commit(smem_addr(&bars.o_full[t]));
-            }
-          }
-          if (t == 1) release(v, 2);
-          if (j + 1 < e[t]) {
-            if (!k_ready) {
-              if (!(ok = wait_boxes(k_next, 3))) break;
-              tc_fence_after();
-              k_ready = true;
-            }
-            scores(t, k_next);
-          }
+          for (int u = 0; u < 12; ++u)
+            mma_ss_pair(st, qd + (u >> 2) * (kBox >> 4) + 2 * (u & 3), kd + (u >> 2) * (kHalfBox >> 4) + 2 * (u & 3),
+                        idesc, u > 0 ? 1u : 0u);
+          mma_commit_pair(smem_addr(&sh.s_full[p.s]));
         }
-        if (ok && j + 1 < t1) release(k_next, 3);
-        nb += 5;
+        if (ok) mma_commit_pair(smem_addr(&sh.q_empty[b]));
       }
-      if (ok && lane == 0) mma_commit(smem_addr(&bars.q_empty));
-    }
-    if (lane == 0) {
-      mma_commit(smem_addr(&bars.done));
-      W.wait(&bars.done, 0, true);
+      mma_commit_pair(smem_addr(&sh.done));
+      W.wait(&sh.done, 0, true);
     }
     __syncwarp();
-  } else {
-    // ------------------------------------------------------------ softmax
-    const int t = warp >> 2;                           // query tile
-    const int row = (warp & 3) * 32 + lane;            // row of the tile = TMEM lane
-    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t st = tmem + lanes + kTmemS + 128 * t, ot = tmem + lanes + kTmemO + 128 * t;
-    int ns = 0;                                        // S tiles consumed = P tiles made
-    bool ok = true;
-    for (; cur.more() && ok; cur.next(a)) {
-      const int t1 = cur.t1(), r0 = cur.qb * kBlockQ + kTile * t;
-      if (threadIdx.x == 0 && cur.t0 == 0 && t1 < cur.tiles) {
-        // the item goes on in the following runs
-        const long long last = (cur.u + cur.tiles - 1) / bars.quota;
-        a.info[blockIdx.x] = SplitInfo{(int)(last - blockIdx.x) + 1, cur.s.q0 + cur.qb * kBlockQ,
-                                       min(cur.s.n - cur.qb * kBlockQ, kBlockQ), cur.h};
+  } else if (warp == 11) {
+    // ------------------------------------------------------------ MMA issuer: values
+    if (rank == 0 && lane == 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(256, 128, 0, 1);
+      RingPos p;
+      int no = 0;
+      bool ok = true;
+      for (; cur.more() && ok; cur.next(a), ++no) {
+        const int t1 = cur.t1();
+        if (!W.wait(&sh.o_empty, (no & 1) ^ 1)) break;
+        for (int j = cur.t0; j < t1; ++j, p.next()) {
+          // the rows cleared by the other CTA's threads want the wider acquire
+          if (!(ok = tail(j) ? W.wait_cluster(&sh.v_full[p.s], p.phase) : W.wait(&sh.v_full[p.s], p.phase))) break;
+          if (!(ok = W.wait(&sh.p_full[p.s], p.phase))) break;
+          tc_fence_after();
+          const uint64_t vd = smem_desc_sw128(stages + p.s * kStageBytes + kKBytes, kBox, 1024);
+          const uint32_t pt = tmem + kTmemS + 128 * p.s;
+#pragma unroll
+          for (int u = 0; u < 8; ++u)  // 16 keys: 8 columns of P, 16 rows of V
+            mma_tmem_a_pair(tmem + kTmemO, pt + 8 * u, vd + 128 * u, idesc, (u > 0 || j > cur.t0) ? 1u : 0u);
+          mma_commit_pair(smem_addr(&sh.o_full[p.s]));
+        }
+        if (ok) mma_commit_pair(smem_addr(&sh.o_done));
       }
-      if (r0 >= cur.s.n) continue;
-      const int e = min(t1, cur.s.tiles(r0 + kTile, a.causal));
+      mma_commit_pair(smem_addr(&sh.done));
+      W.wait(&sh.done, 0, true);
+    }
+    __syncwarp();
+  } else if (warp == 10) {
+    // ------------------------------------------------------------ value rows behind a sequence's end
+    // Their probabilities are 0, but 0 * NaN is NaN: whatever lies there is cleared.
+    RingPos p;
+    uint32_t phases = 0;  // of the entries of v_landed, which only some tiles use
+    for (; cur.more(); cur.next(a)) {
+      const int t1 = cur.t1();
+      for (int j = cur.t0; j < t1 - 1; ++j) p.next();  // only an item's last tile can be its sequence's last
+      if (tail(t1 - 1)) {
+        if (!W.wait_warp(&sh.v_landed[p.s], (phases >> p.s) & 1)) break;
+        phases ^= 1u << p.s;
+        const uint32_t vs = stages + p.s * kStageBytes + kKBytes;
+        for (int x = max(cur.s.L - (t1 - 1) * kTile, 0) * 8 + lane; x < kTile * 8; x += 32)
+          st_shared_v4(vs + 16 * x, make_uint4(0, 0, 0, 0));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_release_cluster(leader(&sh.v_full[p.s]));
+      }
+      p.next();
+    }
+    __syncwarp();
+  } else if (warp < 8) {
+    // ------------------------------------------------------------ softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    const int g = warp >> 2, quad = warp & 3;          // warpgroup, 32-row quadrant
+    const int row = quad * 32 + lane;                  // row of the CTA = TMEM lane
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+    RingPos p, before;                                 // this tile's entry, the previous tile's
+    int turn = 0;                                      // tiles so far, mod 2: whose turn it is
+    int nm = 0, nf = 0, ni = 0;                        // tiles with shared maxima; written items with live rows, all items
+    bool ok = true;
+    // An item whose rows this warp has still to write: its reference maximum and
+    // sum, first output row and head, how its rows are kept.
+    struct Pending {
+      float m, l;
+      int q, h;
+      bool any, live, valid, whole;
+      size_t slot;
+    } pend;
+    pend.any = false;
+    // The rows of an item, or this run's part of them: 64 columns for each
+    // warpgroup. The last P V is normally long done when this is called.
+    const auto write_rows = [&]() {
+      pend.any = false;
+      if (!W.wait_warp(&sh.o_done, ni & 1)) return false;
+      ++ni;
+      tc_fence_after();
+      if (!pend.live) {
+        if (lane == 0) mbar_arrive_cluster(leader(&sh.o_empty));
+        return true;
+      }
+      uint32_t o[2][32];
+      tmem_ld_32x32b_32(lanes + kTmemO + 64 * g, o[0]);
+      tmem_ld_32x32b_32(lanes + kTmemO + 64 * g + 32, o[1]);
+      tmem_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(leader(&sh.o_empty));
+      if (!W.wait_warp(&sh.fin[quad], nf & 1)) return false;
+      const float m1 = sh.fin_m[nf & 1][g ^ 1][row], l1 = sh.fin_l[nf & 1][g ^ 1][row];
+      ++nf;
+      const float mm = fmaxf(pend.m, m1);
+      float l = pend.l > 0.f ? pend.l * ex2((pend.m - mm) * a.scale_log2) : 0.f;
+      if (l1 > 0.f) l += l1 * ex2((m1 - mm) * a.scale_log2);
+      const float inv = l > 0.f ? 1.f / l : 0.f;       // a row without keys: its products are all 0 * v
+      const float lse = l > 0.f ? mm * a.scale + logf(l) : -INFINITY;
+      if (!pend.valid) return true;
+      if (pend.whole) {
+        const size_t r = (size_t)pend.q * a.heads + pend.h;
+        __nv_bfloat16* dst = a.out + r * 128 + 64 * g;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          uint32_t w[8];
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+            w[x] = pack_bf16x2(__uint_as_float(o[u >> 1][16 * (u & 1) + 2 * x]) * inv,
+                               __uint_as_float(o[u >> 1][16 * (u & 1) + 2 * x + 1]) * inv);
+          st_global_v8(dst + 16 * u, w);
+        }
+        if (g == 0) a.lse[r] = lse;
+      } else {
+        const size_t prow = pend.slot * kBlockQ + kTile * rank + row;
+        float* dst = a.part_o + prow * 128 + 64 * g;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          uint32_t w[8];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) w[x] = __float_as_uint(__uint_as_float(o[u >> 2][8 * (u & 3) + x]) * inv);
+          st_global_v8(dst + 8 * u, w);
+        }
+        if (g == 0) a.part_lse[prow] = lse;
+      }
+      return true;
+    };
+    for (; cur.more() && ok; cur.next(a)) {
+      const int t1 = cur.t1(), r0 = cur.qb * kBlockQ + kTile * rank;
+      if (rank == 0 && threadIdx.x == 0 && cur.t0 == 0 && t1 < cur.tiles) {
+        // the item goes on in the following runs
+        const long long last = (cur.u + cur.tiles - 1) / sh.quota;
+        a.info[worker] = SplitInfo{(int)(last - worker) + 1, cur.s.q0 + cur.qb * kBlockQ,
+                                   min(cur.s.n - cur.qb * kBlockQ, kBlockQ), cur.h};
+      }
       const int i = r0 + row;                          // query of the sequence
       const int limit = a.causal ? min(cur.s.L, cur.s.L - cur.s.n + i + 1) : cur.s.L;  // keys it sees
-      float m = -INFINITY, l = 0.f;                    // reference maximum (raw scores), sum of exponentials
-      for (int j = cur.t0; j < e; ++j) {
-        if (!(ok = W.wait_warp(&bars.s_full[t], ns & 1))) break;
+      const bool live = r0 < cur.s.n;                  // without live rows only the hand-shakes remain
+      float m = -INFINITY, l = 0.f;                    // this warpgroup's reference maximum (raw scores) and sum
+      for (int j = cur.t0; j < t1; ++j, turn ^= 1, nm += live) {
+        const RingPos now = p, prev = before;
+        before = p;
+        p.next();
+        if (turn != g) continue;
+        // The rows of the item before are written behind this item's first tile,
+        // whose softmax does not need O, but before any other tile: that one may
+        // have to rescale O, which the tensor cores start on only then.
+        if (j > cur.t0 && pend.any && !(ok = write_rows())) break;
+        if (!(ok = W.wait_warp(&sh.s_full[now.s], now.phase))) break;
         tc_fence_after();
-        uint32_t s[4][32];
+        const uint32_t st = lanes + kTmemS + 128 * now.s;
+        if (live) {
+          uint32_t s[4][32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld_32x32b_32(st + 32 * c, s[c]);
-        tmem_wait_ld();
-        const int seen = limit - j * kTile;
-        if (!__all_sync(~0u, seen >= kTile)) {
+          for (int c = 0; c < 4; ++c) tmem_ld_32x32b_32(st + 32 * c, s[c]);
+          // the reference after the previous tile
+          if (nm > 0 && !(ok = W.wait_warp(&sh.m_ready[quad], (nm - 1) & 1))) break;
+          float m_prev = sh.m[(nm & 1) ^ 1][row];
+          tmem_wait_ld();
+          const int seen = limit - j * kTile;
+          if (!__all_sync(~0u, seen >= kTile)) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+            for (int c = 0; c < 4; ++c)
 #pragma unroll
-            for (int x = 0; x < 32; ++x)
-              if (32 * c + x >= seen) s[c][x] = 0xff800000u;  // -inf
-        }
-        float mx[4];
+              for (int x = 0; x < 32; ++x)
+                if (32 * c + x >= seen) s[c][x] = 0xff800000u;  // -inf
+          }
+          float mx[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          mx[c] = __uint_as_float(s[c][0]);
-#pragma unroll
-          for (int x = 1; x < 31; x += 2) mx[c] = max3(mx[c], __uint_as_float(s[c][x]), __uint_as_float(s[c][x + 1]));
-          mx[c] = fmaxf(mx[c], __uint_as_float(s[c][31]));
-        }
-        const float top = fmaxf(fmaxf(m, fmaxf(mx[0], mx[1])), fmaxf(mx[2], mx[3]));
-        const bool grow = j > cur.t0 && (top - m) * a.scale_log2 > kGrowth;  // false while both are -inf (NaN)
-        if (j == cur.t0) {
-          m = top;
-        } else if (__any_sync(~0u, grow)) {
-          const float f = grow ? ex2((m - top) * a.scale_log2) : 1.f;
-          if (!(ok = W.wait_warp(&bars.o_full[t], (ns - 1) & 1))) break;
-          tc_fence_after();
-#pragma unroll 1
           for (int c = 0; c < 4; ++c) {
-            uint32_t o[32];
-            tmem_ld_32x32b_32(ot + 32 * c, o);
-            tmem_wait_ld();
+            mx[c] = __uint_as_float(s[c][0]);
 #pragma unroll
-            for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-            tmem_st_32(ot + 32 * c, o);
+            for (int x = 1; x < 31; x += 2) mx[c] = max3(mx[c], __uint_as_float(s[c][x]), __uint_as_float(s[c][x + 1]));
+            mx[c] = fmaxf(mx[c], __uint_as_float(s[c][31]));
           }
-          l *= f;
-          if (grow) m = top;
-        }
-        const float shift = m == -INFINITY ? 0.f : -m * a.scale_log2;
-        const float2 k2 = make_float2(a.scale_log2, a.scale_log2), b2 = make_float2(shift, shift);
-        float2 sum[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          sum[c] = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int x = 0; x < 32; x += 2) {
-            const float2 y = fma2_rn(make_float2(__uint_as_float(s[c][x]), __uint_as_float(s[c][x + 1])), k2, b2);
-            const float2 p = make_float2(ex2(y.x), ex2(y.y));
-            sum[c] = add2_rn(sum[c], p);
-            s[c >> 1][(c & 1) * 16 + x / 2] = pack_bf16x2(p.x, p.y);
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          if (j == cur.t0) m_prev = top;
+          const bool grow = (top - m_prev) * a.scale_log2 > kGrowth;  // false while both are -inf (NaN)
+          const float m_new = grow ? top : m_prev;
+          sh.m[nm & 1][row] = m_new;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&sh.m_ready[quad]));
+          if (m_new != m) {
+            l *= ex2((m - m_new) * a.scale_log2);      // 0 * ex2(-inf) at the first
+            m = m_new;
           }
-          if (c & 1) tmem_st_32(st + 32 * (c >> 1), s[c >> 1]);
+          if (__any_sync(~0u, grow)) {
+            const float f = grow ? ex2((m_prev - m_new) * a.scale_log2) : 1.f;
+            if (!(ok = W.wait_warp(&sh.o_full[prev.s], prev.phase))) break;  // the previous tile's P V
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t o[32];
+              tmem_ld_32x32b_32(lanes + kTmemO + 32 * c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+              tmem_st_32(lanes + kTmemO + 32 * c, o);
+            }
+          }
+          const float shift = m == -INFINITY ? 0.f : -m * a.scale_log2;
+          const float2 k2 = make_float2(a.scale_log2, a.scale_log2), b2 = make_float2(shift, shift);
+          float2 sum[4];
+          uint32_t p0[32], p1[32];
+          const auto exponentials = [&](const uint32_t(&x)[32], uint32_t* out, float2& total) {
+            total = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int u = 0; u < 32; u += 2) {
+              const float2 y = fma2_rn(make_float2(__uint_as_float(x[u]), __uint_as_float(x[u + 1])), k2, b2);
+              const float2 e2 = make_float2(ex2(y.x), ex2(y.y));
+              total = add2_rn(total, e2);
+              out[u / 2] = pack_bf16x2(e2.x, e2.y);
+            }
+          };
+          exponentials(s[0], p0, sum[0]);
+          exponentials(s[1], p0 + 16, sum[1]);
+          tmem_st_32(st, p0);
+          exponentials(s[2], p1, sum[2]);
+          exponentials(s[3], p1 + 16, sum[3]);
+          tmem_st_32(st + 32, p1);
+          const float2 s01 = add2_rn(add2_rn(sum[0], sum[1]), add2_rn(sum[2], sum[3]));
+          l += s01.x + s01.y;
+          tmem_wait_st();
         }
-        const float2 s01 = add2_rn(add2_rn(sum[0], sum[1]), add2_rn(sum[2], sum[3]));
-        l += s01.x + s01.y;
-        tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&bars.p_full[t]));
-        ++ns;
+        if (lane == 0) mbar_arrive_cluster(leader(&sh.p_full[now.s]));
+        if (pend.any && !(ok = write_rows())) break;
       }
-      if (!ok) break;
-      // finished rows, or this run's part of them
-      const bool whole = cur.t0 == 0 && t1 == cur.tiles;
-      const bool valid = i < cur.s.n;
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      const float lse = l > 0.f ? m * a.scale + logf(l) : -INFINITY;
-      const size_t slot = (size_t)2 * blockIdx.x + (cur.t0 == 0 ? 1 : 0);
-      const int prow = kTile * t + row;
-      __nv_bfloat16* dst = a.out + ((size_t)(cur.s.q0 + i) * a.heads + cur.h) * 128;
-      float* part = a.part_o + (slot * kBlockQ + prow) * 128;
-      if (cur.t0 < e) {
-        if (!(ok = W.wait_warp(&bars.o_full[t], (ns - 1) & 1))) break;
-        tc_fence_after();
-      }
-#pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        uint32_t o[32];
-        if (cur.t0 < e) {
-          tmem_ld_32x32b_32(ot + 32 * c, o);
-          tmem_wait_ld();
-        } else {
-#pragma unroll
-          for (int x = 0; x < 32; ++x) o[x] = 0u;
-        }
-        if (!valid) continue;
-        // a row without keys: its products are all 0 * v
-        if (whole) {
-          uint4* d4 = reinterpret_cast<uint4*>(dst + 32 * c);
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            uint32_t w[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              w[x] = pack_bf16x2(__uint_as_float(o[8 * u + 2 * x]) * inv, __uint_as_float(o[8 * u + 2 * x + 1]) * inv);
-            d4[u] = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        } else {
-          float4* d4 = reinterpret_cast<float4*>(part + 32 * c);
-#pragma unroll
-          for (int u = 0; u < 8; ++u)
-            d4[u] = make_float4(__uint_as_float(o[4 * u]) * inv, __uint_as_float(o[4 * u + 1]) * inv,
-                                __uint_as_float(o[4 * u + 2]) * inv, __uint_as_float(o[4 * u + 3]) * inv);
-        }
-      }
-      if (valid) {
-        if (whole) a.lse[(size_t)(cur.s.q0 + i) * a.heads + cur.h] = lse;
-        else a.part_lse[slot * kBlockQ + prow] = lse;
+      if (!ok || (pend.any && !(ok = write_rows()))) break;
+      pend.any = true;
+      pend.live = live;
+      if (live) {
+        const int f = nf & 1;  // the item before is written: this is item nf
+        sh.fin_m[f][g][row] = m;
+        sh.fin_l[f][g][row] = l;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sh.fin[quad]));
+        pend.m = m;
+        pend.l = l;
+        pend.q = cur.s.q0 + i;
+        pend.h = cur.h;
+        pend.valid = i < cur.s.n;
+        pend.whole = cur.t0 == 0 && t1 == cur.tiles;
+        pend.slot = (size_t)2 * worker + (cur.t0 == 0 ? 1 : 0);
       }
     }
+    if (ok && pend.any) write_rows();
     __syncwarp();
   }
 
   allow_dependents();  // the merge kernel's blocks may take SMs as these CTAs finish
   tc_fence_before();
-  __syncthreads();
-  if (warp == 8) {
-    tc_fence_after();
-    tmem_dealloc(tmem, kTmemAll);
-  }
+  cluster_sync();      // neither CTA leaves while the other may still reach its shared memory or TMEM
+  tc_fence_after();
+  if (warp == 8) tmem_dealloc_pair(tmem, kTmemAll);
 }
 
 // Merge of split items: block (w, g) joins 16 rows of the item that run w
@@ -599,7 +719,7 @@ mla_status_t check_attention(const mlap_attention_desc_t* d) {
   return MLA_OK;
 }
 
-// Workers (one per SM) of the current device for this descriptor; 0 on a CUDA error.
+// Workers (CTA pairs) of the current device for this descriptor; 0 on a CUDA error.
 int attention_workers(const mlap_attention_desc_t* d) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -607,7 +727,8 @@ int attention_workers(const mlap_attention_desc_t* d) {
     cudaGetLastError();
     return 0;
   }
-  return d->num_sms > 0 && d->num_sms < sms ? d->num_sms : sms;
+  if (d->num_sms > 0 && d->num_sms < sms) sms = d->num_sms;
+  return sms < 2 ? 1 : sms / 2;
 }
 
 // Workspace: [SplitInfo | part_lse | part_o], each a multiple of 256 bytes.
@@ -617,13 +738,16 @@ size_t workspace_bytes(int workers) {
   return info_bytes(workers) + part_lse_bytes(workers) + (size_t)2 * workers * kBlockQ * 128 * sizeof(float);
 }
 
-bool encode_rows(CUtensorMap* m, const void* p, long long cols, long long rows, long long stride) {
+// A row-major bf16 matrix as [64 columns, rows, 64-column blocks]; a box's
+// blocks lie one after the other, rows 128-byte swizzled.
+bool encode_blocks(CUtensorMap* m, const void* p, long long blocks, long long rows, long long stride, int box_rows,
+                   int box_blocks) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
   if (!enc) return false;
-  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)stride * 2};
-  cuuint32_t box[2] = {64, kTile}, elem[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides, box, elem,
+  cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)blocks};
+  cuuint64_t strides[2] = {(cuuint64_t)stride * 2, 128};
+  cuuint32_t box[3] = {64, (cuuint32_t)box_rows, (cuuint32_t)box_blocks}, elem[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, elem,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -636,7 +760,7 @@ mla_status_t attention(const mlap_attention_desc_t* d, const void* q, const void
   if (d->batch == 0 || d->num_q == 0) return MLA_OK;
   if (!q || !cu_q || !cu_k || !out || !lse || !workspace || (d->num_k > 0 && (!kv || !k_pe))) return MLA_ERR_INVALID_ARG;
   const auto off = [](const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) != 0; };
-  if (off(q, 16) || off(kv, 16) || off(k_pe, 16) || off(out, 16) || off(workspace, 16) || off(cu_q, 4) ||
+  if (off(q, 16) || off(kv, 16) || off(k_pe, 16) || off(out, 32) || off(workspace, 32) || off(cu_q, 4) ||
       off(cu_k, 4) || off(lse, 4) || off(error, 4))
     return MLA_ERR_INVALID_ARG;
   const int workers = attention_workers(d);
@@ -645,10 +769,12 @@ mla_status_t attention(const mlap_attention_desc_t* d, const void* q, const void
   AttnMaps maps;
   // without keys the boxes still load (all masked): any valid memory does
   const bool keys = d->num_k > 0;
-  if (!encode_rows(&maps.q, q, (long long)d->num_heads * 192, d->num_q, (long long)d->num_heads * 192) ||
-      !encode_rows(&maps.kv, keys ? kv : q, keys ? (long long)d->num_heads * 256 : 64, keys ? d->num_k : 1,
-                   keys ? (long long)d->num_heads * 256 : 64) ||
-      !encode_rows(&maps.pe, keys ? k_pe : q, 64, keys ? d->num_k : 1, keys ? d->pe_stride : 64))
+  const void* kvp = keys ? kv : q;
+  const long long kv_blocks = keys ? 4ll * d->num_heads : 1, nk = keys ? d->num_k : 1;
+  if (!encode_blocks(&maps.q, q, 3ll * d->num_heads, d->num_q, 192ll * d->num_heads, kTile, 3) ||
+      !encode_blocks(&maps.k, kvp, kv_blocks, nk, 64 * kv_blocks, kTile / 2, 2) ||
+      !encode_blocks(&maps.v, kvp, kv_blocks, nk, 64 * kv_blocks, kTile, 1) ||
+      !encode_blocks(&maps.pe, keys ? k_pe : q, 1, nk, keys ? d->pe_stride : 64, kTile / 2, 1))
     return MLA_ERR_CUDA;
   AttnArgs a;
   a.cu_q = cu_q;
@@ -671,7 +797,7 @@ mla_status_t attention(const mlap_attention_desc_t* d, const void* q, const void
   if (cudaFuncSetAttribute((const void*)mla_prefill_attention_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            kAttnSmem) != cudaSuccess)
     return MLA_ERR_CUDA;
-  mla_prefill_attention_kernel<<<workers, kAttnThreads, kAttnSmem, stream>>>(maps, a);
+  mla_prefill_attention_kernel<<<2 * workers, kAttnThreads, kAttnSmem, stream>>>(maps, a);
   if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(workers, kBlockQ / kMergeRows, 1);

@@ -31,18 +31,24 @@ struct Waiter {
     *reinterpret_cast<volatile uint32_t*>(abort_flag) = 1u;
     set_error(err, kErrTimeout);
   }
-  MLA_DEV bool wait(uint64_t* bar, uint32_t parity, bool drain = false) {
+  template <bool kCluster>
+  MLA_DEV bool wait_impl(uint64_t* bar, uint32_t parity, bool drain) {
     const uint32_t a = smem_addr(bar);
-    if (mbar_try_wait(a, parity)) return true;
+    if (kCluster ? mbar_try_wait_cluster(a, parity) : mbar_try_wait(a, parity)) return true;
     const uint64_t t0 = global_timer_ns();
     while (true) {
-      if (mbar_try_wait(a, parity)) return true;
+      if (kCluster ? mbar_try_wait_cluster(a, parity) : mbar_try_wait(a, parity)) return true;
       if (!drain && aborted()) return false;
       if (global_timer_ns() - t0 > kWaitNs) {
         fail();
         return false;
       }
     }
+  }
+  MLA_DEV bool wait(uint64_t* bar, uint32_t parity, bool drain = false) { return wait_impl<false>(bar, parity, drain); }
+  // For phases completed by the other CTA of a pair.
+  MLA_DEV bool wait_cluster(uint64_t* bar, uint32_t parity, bool drain = false) {
+    return wait_impl<true>(bar, parity, drain);
   }
   // Every lane waits; the outcome is made warp-uniform so that no lane leaves
   // a loop its warp-mates stay in.

@@ -103,20 +103,20 @@ def _attn(libmla, **kw):
 def test_attention_bad_descriptors_rejected(libmla, kw, status):
     d = _attn(libmla, **kw)
     assert libmla.mlap_attention_workspace_bytes(d) == 0
-    assert libmla.mlap_attention(d, *([16] * 8), 1 << 40, None, None) == status
+    assert libmla.mlap_attention(d, *([32] * 8), 1 << 40, None, None) == status
 
 
 def test_attention_null_misaligned_and_empty(libmla):
     INV = libmla.MLA_ERR_INVALID_ARG
     for i in range(8):
-        a = [16] * 8
+        a = [32] * 8
         a[i] = None
         assert libmla.mlap_attention(_attn(libmla), *a, 1 << 40, None, None) == INV, i
-    for i, off in enumerate((8, 8, 8, 2, 2, 8, 2, 8)):
-        a = [16] * 8
+    for i, off in enumerate((8, 8, 8, 2, 2, 16, 2, 16)):
+        a = [32] * 8
         a[i] += off
         assert libmla.mlap_attention(_attn(libmla), *a, 1 << 40, None, None) == INV, i
-    assert libmla.mlap_attention(_attn(libmla), *([16] * 8), 1 << 40, 18, None) == INV
+    assert libmla.mlap_attention(_attn(libmla), *([32] * 8), 1 << 40, 18, None) == INV
     for kw in (dict(batch=0), dict(num_q=0)):
         assert libmla.mlap_attention(_attn(libmla, **kw), *([None] * 8), 0, None, None) == libmla.MLA_OK
 
@@ -124,7 +124,7 @@ def test_attention_null_misaligned_and_empty(libmla):
 def test_attention_causal_flag_outside_0_1_rejected(libmla):
     d = _attn(libmla)
     d.causal = 2
-    assert libmla.mlap_attention(d, *([16] * 8), 1 << 40, None, None) == libmla.MLA_ERR_INVALID_ARG
+    assert libmla.mlap_attention(d, *([32] * 8), 1 << 40, None, None) == libmla.MLA_ERR_INVALID_ARG
 
 
 def test_merge_takes_both_widths(libmla):
