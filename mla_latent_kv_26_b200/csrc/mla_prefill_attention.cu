@@ -21,13 +21,14 @@
 // A CTA pair (cta_group::2) works on a block: S = Q K^T and O += P V with M 256,
 // 128 rows in each CTA. Each CTA loads half of every key tile (64 keys of K,
 // 64 columns of V), so that a tile costs the pair's SMs 40 KB each and three
-// tiles fit beside two Q buffers. TMEM of a CTA: O (128 columns) and three S
-// buffers; P (bf16) overwrites the lower half of its S. The scores run up
-// to three tiles ahead of the values, S(i + 3) behind P(i) V(i), and the two
-// softmax warpgroups of a CTA take alternate tiles: neither the tensor cores nor
-// the exponentials wait for one another's latency. (One CTA with two query
-// tiles and one S buffer each has the tensor cores idle for the whole chain of
-// S, softmax, P V; it took 4400 cycles per 2560 of products.)
+// tiles fit beside two Q buffers. TMEM of a CTA: O (128 columns), two S buffers
+// of 128 and two P buffers (bf16) of 64. The two softmax warpgroups of a CTA take
+// alternate tiles, one S and one P buffer each. A warpgroup frees its S as soon as
+// it holds the scores in registers, so that the tensor cores make its next S
+// while it works on this one, and P V follows when it comes: neither waits for
+// the other's latency. (With P over S and three S buffers the loop S, softmax,
+// P V, S bound: 1800 cycles a tile for 1280 of products. One CTA with two query
+// tiles of one S each: 4400 cycles per 2560.)
 //
 // Per CTA (384 threads):
 //   warps 0-3, 4-7  softmax of the even / odd key tiles, one thread per row: S
@@ -59,14 +60,14 @@ namespace prefill {
 constexpr int kAttnThreads = 384;
 constexpr int kTile = 128;                 // query rows of a CTA, keys of a key tile
 constexpr int kBlockQ = 2 * kTile;         // queries of an item
-constexpr int kStages = 3;                 // key tiles in shared memory, and S buffers
+constexpr int kStages = 3;                 // key tiles in shared memory
 constexpr int kQBytes = 3 * kBox;          // 128 rows x 192
 constexpr int kHalfBox = kBox / 2;         // 64 rows x 64 columns
 constexpr int kKBytes = 3 * kHalfBox;      // 64 keys x 192 (two column blocks of K, k_pe)
 constexpr int kVBytes = kBox;              // 128 keys x 64
 constexpr int kStageBytes = kKBytes + kVBytes;
 constexpr int kAttnSmem = 1024 + 2 * kQBytes + kStages * kStageBytes;
-constexpr uint32_t kTmemO = 0, kTmemS = 128, kTmemAll = 512;
+constexpr uint32_t kTmemO = 0, kTmemP = 128, kTmemS = 256, kTmemAll = 512;
 constexpr float kGrowth = 8.0f;            // log2: O is rescaled when a row's maximum grew by more (p stays below 2^8)
 // Registers a thread after the split: the softmax warpgroups hold a row of
 // scores each. 256 * 200 + 128 * 104 = 64512 = the 384 * 168 launched.
@@ -242,10 +243,13 @@ struct PendingRows {
 };
 
 struct AttnShared {
-  // key tile i uses entry i % 3; the even CTA's entries serve both CTAs
-  uint64_t k_full[kStages], v_full[kStages];   // even CTA: both CTAs' halves have landed
-  uint64_t p_full[kStages];                    // even CTA: the P of both CTAs' rows
-  uint64_t s_full[kStages], o_full[kStages];   // both: Q K(i)^T / P(i) V(i) done, so K(i) / V(i) may be overwritten
+  // Key tile i uses entry i % 3 of the first four, i % 2 of the next three.
+  // "even": only the even CTA's is used, by both CTAs; "both": each CTA's own.
+  uint64_t k_full[kStages], v_full[kStages];   // even: both CTAs' halves have landed
+  uint64_t k_empty[kStages];                   // both: Q K(i) done
+  uint64_t pv_done[kStages];                   // both: P(i) V(i) done
+  uint64_t s_full[2];                          // both: Q K(i) done
+  uint64_t s_free[2], p_full[2];               // even: scores read, probabilities written by both CTAs
   uint64_t q_full[2], q_empty[2];              // q_full: even CTA
   uint64_t o_done;                             // both: an item's last P V is done
   uint64_t o_empty;                            // even CTA: both CTAs have read an item's O
@@ -270,6 +274,11 @@ struct RingPos {
       s = 0;
       phase ^= 1u;
     }
+  }
+  MLA_DEV void advance(int n) {
+    s += n;
+    phase ^= (uint32_t)(s / kStages) & 1u;
+    s %= kStages;
   }
 };
 
@@ -301,12 +310,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     for (int s = 0; s < kStages; ++s) {
       mbar_init(smem_addr(&sh.k_full[s]), 2);  // both producers, or both clearing warps
       mbar_init(smem_addr(&sh.v_full[s]), 2);
-      mbar_init(smem_addr(&sh.p_full[s]), 8);  // four softmax warps of either CTA
-      mbar_init(smem_addr(&sh.s_full[s]), 1);
-      mbar_init(smem_addr(&sh.o_full[s]), 1);
+      mbar_init(smem_addr(&sh.k_empty[s]), 1);
+      mbar_init(smem_addr(&sh.pv_done[s]), 1);
       mbar_init(smem_addr(&sh.v_landed[s]), 1);
     }
     for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_addr(&sh.s_full[b]), 1);
+      mbar_init(smem_addr(&sh.s_free[b]), 8);  // four softmax warps of either CTA
+      mbar_init(smem_addr(&sh.p_full[b]), 8);
       mbar_init(smem_addr(&sh.q_full[b]), 2);
       mbar_init(smem_addr(&sh.q_empty[b]), 1);
     }
@@ -365,7 +376,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
                            leader(&sh.q_full[b]));
           ++nq;
         }
-        if (!W.wait(&sh.s_full[pk.s], pk.phase ^ 1)) return false;  // K of three tiles ago is done with
+        if (!W.wait(&sh.k_empty[pk.s], pk.phase ^ 1)) return false;  // K of three tiles ago is done with
         const uint32_t kf = leader(&sh.k_full[pk.s]), ks = stages + pk.s * kStageBytes;
         const int row = ahead.s.k0 + jk * kTile + 64 * rank;
         mbar_arrive_expect_tx_cluster(kf, kKBytes);
@@ -382,7 +393,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
       for (; cur.more() && ok; cur.next(a)) {
         const int t1 = cur.t1();
         for (int j = cur.t0; j < t1; ++j, pv.next()) {
-          if (!(ok = W.wait(&sh.o_full[pv.s], pv.phase ^ 1))) break;  // V of three tiles ago is done with
+          if (!(ok = W.wait(&sh.pv_done[pv.s], pv.phase ^ 1))) break;  // V of three tiles ago is done with
           const uint32_t vs = stages + pv.s * kStageBytes + kKBytes;
           const int row = cur.s.k0 + j * kTile;
           if (tail(j)) {
@@ -410,24 +421,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     if (rank == 0 && lane == 0) {
       constexpr uint32_t idesc = idesc_bf16_f32(256, 128, 0, 0);
       RingPos p;
-      int nq = 0;
+      int nq = 0, i = 0;  // query blocks, tiles
       bool ok = true;
       for (; cur.more() && ok; cur.next(a), ++nq) {
         const int t1 = cur.t1(), b = nq & 1;
         if (!W.wait(&sh.q_full[b], (nq >> 1) & 1)) break;
         const uint64_t qd = smem_desc_sw128(qbuf + b * kQBytes, 16, 1024);
-        for (int j = cur.t0; j < t1; ++j, p.next()) {
+        for (int j = cur.t0; j < t1; ++j, p.next(), ++i) {
           if (!(ok = W.wait(&sh.k_full[p.s], p.phase))) break;
-          if (!(ok = W.wait(&sh.o_full[p.s], p.phase ^ 1))) break;  // P V of three tiles ago has read this S entry
+          if (!(ok = W.wait(&sh.s_free[i & 1], ((i >> 1) & 1) ^ 1))) break;
           tc_fence_after();
           // S = Q K^T; 16 columns are 32 bytes of a swizzled row
           const uint64_t kd = smem_desc_sw128(stages + p.s * kStageBytes, 16, 1024);
-          const uint32_t st = tmem + kTmemS + 128 * p.s;
+          const uint32_t st = tmem + kTmemS + 128 * (i & 1);
 #pragma unroll
           for (int u = 0; u < 12; ++u)
             mma_ss_pair(st, qd + (u >> 2) * (kBox >> 4) + 2 * (u & 3), kd + (u >> 2) * (kHalfBox >> 4) + 2 * (u & 3),
                         idesc, u > 0 ? 1u : 0u);
-          mma_commit_pair(smem_addr(&sh.s_full[p.s]));
+          mma_commit_pair(smem_addr(&sh.s_full[i & 1]));
+          mma_commit_pair(smem_addr(&sh.k_empty[p.s]));
         }
         if (ok) mma_commit_pair(smem_addr(&sh.q_empty[b]));
       }
@@ -440,22 +452,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     if (rank == 0 && lane == 0) {
       constexpr uint32_t idesc = idesc_bf16_f32(256, 128, 0, 1);
       RingPos p;
-      int no = 0;
+      int no = 0, i = 0;  // items, tiles
       bool ok = true;
       for (; cur.more() && ok; cur.next(a), ++no) {
         const int t1 = cur.t1();
         if (!W.wait(&sh.o_empty, (no & 1) ^ 1)) break;
-        for (int j = cur.t0; j < t1; ++j, p.next()) {
+        for (int j = cur.t0; j < t1; ++j, p.next(), ++i) {
           // the rows cleared by the other CTA's threads want the wider acquire
           if (!(ok = tail(j) ? W.wait_cluster(&sh.v_full[p.s], p.phase) : W.wait(&sh.v_full[p.s], p.phase))) break;
-          if (!(ok = W.wait(&sh.p_full[p.s], p.phase))) break;
+          if (!(ok = W.wait(&sh.p_full[i & 1], (i >> 1) & 1))) break;
           tc_fence_after();
           const uint64_t vd = smem_desc_sw128(stages + p.s * kStageBytes + kKBytes, kBox, 1024);
-          const uint32_t pt = tmem + kTmemS + 128 * p.s;
+          const uint32_t pt = tmem + kTmemP + 64 * (i & 1);
 #pragma unroll
           for (int u = 0; u < 8; ++u)  // 16 keys: 8 columns of P, 16 rows of V
             mma_tmem_a_pair(tmem + kTmemO, pt + 8 * u, vd + 128 * u, idesc, (u > 0 || j > cur.t0) ? 1u : 0u);
-          mma_commit_pair(smem_addr(&sh.o_full[p.s]));
+          mma_commit_pair(smem_addr(&sh.pv_done[p.s]));
         }
         if (ok) mma_commit_pair(smem_addr(&sh.o_done));
       }
@@ -490,8 +502,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     const int g = warp >> 2, quad = warp & 3;          // warpgroup, 32-row quadrant
     const int row = quad * 32 + lane;                  // row of the CTA = TMEM lane
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
-    RingPos p, before;                                 // this tile's entry, the previous tile's
-    int turn = 0;                                      // tiles so far, mod 2: whose turn it is
+    const uint32_t st = lanes + kTmemS + 128 * g, pt = lanes + kTmemP + 64 * g;
+    RingPos first;                                     // entry of the item's first tile
+    RingPos mine;                                      // entry of this warpgroup's last tile
+    int turn = 0;                                      // tiles before the item, mod 2
+    int ns = 0;                                        // tiles of this warpgroup
     int nm = 0, nf = 0, ni = 0;                        // tiles with shared maxima; written items with live rows, all items
     bool ok = true;
     bool pending = false;                              // an item's rows are still to be written
@@ -553,9 +568,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
       }
       return true;
     };
-    while (at.more() && ok) {
-      const int t0 = at.t0, t1 = at.t1(), r0 = at.qb * kBlockQ + kTile * rank;
-      if (rank == 0 && threadIdx.x == 0 && t0 == 0 && t1 < at.tiles) {
+    while (true) {
+      const bool more = at.more();
+      if (!more && !pending) break;
+      const int t0 = more ? at.t0 : 0, t1 = more ? at.t1() : 0, r0 = at.qb * kBlockQ + kTile * rank;
+      if (rank == 0 && threadIdx.x == 0 && more && t0 == 0 && t1 < at.tiles) {
         // the item goes on in the following runs
         const long long last = (at.u + at.tiles - 1) / at.quota;
         a.info[worker] = SplitInfo{(int)(last - worker) + 1, at.s.q0 + at.qb * kBlockQ,
@@ -563,30 +580,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
       }
       // keys this row sees
       const int limit = a.causal ? min(at.s.L, at.s.L - at.s.n + r0 + row + 1) : at.s.L;
+      // key tiles that all of the warp's rows see whole (the first row sees least)
+      const int whole_tiles = __shfl_sync(~0u, limit, 0) >> 7;
       const bool live = r0 < at.s.n;                   // without live rows only the hand-shakes remain
       float m = -INFINITY, l = 0.f;                    // this warpgroup's reference maximum (raw scores) and sum
-      for (int j = t0; j < t1; ++j, turn ^= 1, nm += live) {
-        const RingPos now = p, prev = before;
-        before = p;
-        p.next();
-        if (turn != g) continue;
-        // The rows of the item before are written behind this item's first tile,
-        // whose softmax does not need O, but before any other tile: that one may
-        // have to rescale O, which the tensor cores start on only then.
-        if (j > t0 && pending && !(ok = write_rows())) break;
-        if (!(ok = W.wait_warp(&sh.s_full[now.s], now.phase))) break;
+      // This warpgroup's tiles, every second one, and one turn behind the last.
+      // The rows of the item before are written when the item's first tile is
+      // under way: its softmax does not need O, but any other tile may have to
+      // rescale O, which the tensor cores start on only when it has been read.
+      RingPos now = first;
+      if (turn != g) now.next();
+      for (int j = t0 + (turn ^ g);; j += 2) {
+        if (pending && (j > t0 || !more) && !(ok = write_rows())) break;
+        if (j >= t1) break;
+        if (!(ok = W.wait_warp(&sh.s_full[g], ns & 1))) break;
         tc_fence_after();
-        const uint32_t st = lanes + kTmemS + 128 * now.s;
         if (live) {
           uint32_t s[4][32];
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_ld_32x32b_32(st + 32 * c, s[c]);
           // the reference after the previous tile
-          if (nm > 0 && !(ok = W.wait_warp(&sh.m_ready[quad], (nm - 1) & 1))) break;
-          float m_prev = sh.m[(nm & 1) ^ 1][row];
+          const int nt = nm + j - t0;                  // tiles with shared maxima before this one
+          if (nt > 0 && !(ok = W.wait_warp(&sh.m_ready[quad], (nt - 1) & 1))) break;
+          float m_prev = sh.m[(nt & 1) ^ 1][row];
           tmem_wait_ld();
-          const int seen = limit - j * kTile;
-          if (!__all_sync(~0u, seen >= kTile)) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(leader(&sh.s_free[g]));
+          if (j >= whole_tiles) {
+            const int seen = limit - j * kTile;
 #pragma unroll
             for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -605,7 +627,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
           if (j == t0) m_prev = top;
           const bool grow = (top - m_prev) * a.scale_log2 > kGrowth;  // false while both are -inf (NaN)
           const float m_new = grow ? top : m_prev;
-          sh.m[nm & 1][row] = m_new;
+          sh.m[nt & 1][row] = m_new;
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_addr(&sh.m_ready[quad]));
           if (m_new != m) {
@@ -614,7 +636,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
           }
           if (__any_sync(~0u, grow)) {
             const float f = grow ? ex2((m_prev - m_new) * a.scale_log2) : 1.f;
-            if (!(ok = W.wait_warp(&sh.o_full[prev.s], prev.phase))) break;  // the previous tile's P V
+            RingPos prev = now;                        // the previous tile's entry is two further in the ring of three
+            prev.next();
+            prev.next();
+            if (!(ok = W.wait_warp(&sh.pv_done[prev.s], prev.phase ^ 1))) break;
             tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
@@ -642,20 +667,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
           };
           exponentials(s[0], p0, sum[0]);
           exponentials(s[1], p0 + 16, sum[1]);
-          tmem_st_32(st, p0);
+          // P V of this warpgroup's last tile has read its P
+          if (ns > 0 && !(ok = W.wait_warp(&sh.pv_done[mine.s], mine.phase))) break;
+          tc_fence_after();
+          tmem_st_32(pt, p0);
           exponentials(s[2], p1, sum[2]);
           exponentials(s[3], p1 + 16, sum[3]);
-          tmem_st_32(st + 32, p1);
+          tmem_st_32(pt + 32, p1);
           const float2 s01 = add2_rn(add2_rn(sum[0], sum[1]), add2_rn(sum[2], sum[3]));
           l += s01.x + s01.y;
           tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+        } else {
+          if (lane == 0) mbar_arrive_cluster(leader(&sh.s_free[g]));
+          if (ns > 0 && !(ok = W.wait_warp(&sh.pv_done[mine.s], mine.phase))) break;
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(leader(&sh.p_full[now.s]));
-        if (pending && !(ok = write_rows())) break;
+        if (lane == 0) mbar_arrive_cluster(leader(&sh.p_full[g]));
+        mine = now;
+        ++ns;
+        now.next();
+        now.next();
       }
-      if (!ok || (pending && !(ok = write_rows()))) break;
+      if (!ok || !more) break;
+      first.advance(t1 - t0);
+      turn ^= (t1 - t0) & 1;
+      if (live) nm += t1 - t0;
       pending = true;
       __syncwarp();
       if (live) {
@@ -676,7 +713,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
       at = next;
       __syncwarp();
     }
-    if (ok && pending) write_rows();
     __syncwarp();
   }
 
