@@ -8,7 +8,9 @@
 // one pass over the keys; when m grows, o and l are scaled by exp(m_old - m).
 //
 // Work. An item is (sequence, block of 256 queries, head); its units are its
-// visible 128-key tiles. All units are laid end to end and cut into one equal
+// visible 128-key tiles, and kItemUnits more for what an item costs beside its
+// tiles (Q, filling the pipeline, its rows; without them the runs of six prompts
+// of 645 to 1491 tokens took from 52 to 93 us). All units are laid end to end and cut into one equal
 // run per CTA pair, so that every SM gets the same work whatever the lengths.
 // The order is (sequence, group of heads, block, head of the group, tile), with
 // groups of about as many heads as a run has items: pairs then work on the
@@ -69,6 +71,7 @@ constexpr int kStageBytes = kKBytes + kVBytes;
 constexpr int kAttnSmem = 1024 + 2 * kQBytes + kStages * kStageBytes;
 constexpr uint32_t kTmemO = 0, kTmemP = 128, kTmemS = 256, kTmemAll = 512;
 constexpr float kGrowth = 8.0f;            // log2: O is rescaled when a row's maximum grew by more (p stays below 2^8)
+constexpr int kItemUnits = 3;              // cost of an item beside its tiles, in tiles
 // Registers a thread after the split: the softmax warpgroups hold a row of
 // scores each. 256 * 200 + 128 * 104 = 64512 = the 384 * 168 launched.
 constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;
@@ -117,9 +120,12 @@ struct Seq {
   // key tiles worked on for queries below `rows`: at least one, so that rows
   // without keys are written too
   MLA_DEV int tiles(int rows, int causal) const { return max(1, ceil_tiles(visible(rows, causal))); }
-  // tiles of the first m blocks of one head. Causal block x (from 1) short of
+  // units of the first m blocks of one head. Causal block x (from 1) short of
   // the last has max(1, c + 2x) tiles, c = ceil((L - n) / 128): the first
   // k = max(0, -c / 2) of them one each, the others an arithmetic series.
+  MLA_DEV long long units_before(int m, int causal) const {
+    return tiles_before(m, causal) + (long long)m * kItemUnits;
+  }
   MLA_DEV long long tiles_before(int m, int causal) const {
     if (m <= 0) return 0;
     const int last = tiles(n, causal);
@@ -131,24 +137,29 @@ struct Seq {
   }
 };
 
-// Position of a run in the list of items.
+// Position of a run in the list of items. An item takes kItemUnits + tiles units
+// from `item` on; a run that begins or ends in the first kItemUnits begins with,
+// or ends before, the item's first tile.
 struct Cursor {
-  long long u, end;  // next unit, end of the run
-  long long quota;   // units of a run
+  long long item, end;  // the item's first unit, the run's end
+  long long quota;      // units of a run
   Seq s;
   int b, qb, h, t0, tiles;
-  int group;         // heads of a group
-  MLA_DEV bool more() const { return u < end; }
-  MLA_DEV int t1() const { return (int)min((long long)tiles, t0 + (end - u)); }
+  int group;            // heads of a group
+  MLA_DEV int t1() const { return (int)max(0ll, min((long long)tiles, end - item - kItemUnits)); }
+  MLA_DEV bool more() const { return t0 < t1(); }
   // Heads of a group: about a run's number of items of this sequence.
   MLA_DEV static int group_heads(const AttnArgs& a, const Seq& s, long long quota) {
-    const long long per_head = s.tiles_before(s.blocks(), a.causal);
+    const long long per_head = s.units_before(s.blocks(), a.causal);
     return (int)min((long long)a.heads, max(1ll, (quota * s.blocks() + per_head / 2) / max(per_head, 1ll)));
   }
   MLA_DEV void next(const AttnArgs& a) {
-    u += t1() - t0;
+    item += kItemUnits + tiles;
     t0 = 0;
-    if (!more()) return;
+    if (item + kItemUnits >= end) {  // the run ends before this item's first tile
+      tiles = 0;
+      return;
+    }
     const int g0 = h - h % group;
     if (++h < min(g0 + group, a.heads)) return;
     if (++qb < s.blocks()) {
@@ -176,7 +187,7 @@ MLA_DEV void run_start(const AttnArgs& a, int w, Cursor* cur) {
   for (int b = lane; b < a.batch; b += 32) {
     Seq s;
     s.load(a, b);
-    total += s.tiles_before(s.blocks(), a.causal) * a.heads;
+    total += s.units_before(s.blocks(), a.causal) * a.heads;
     const int oq = __ldg(a.cu_q + b), ok = __ldg(a.cu_k + b);
     bad |= oq != s.q0 || ok != s.k0 || __ldg(a.cu_q + b + 1) != s.q0 + s.n || __ldg(a.cu_k + b + 1) != s.k0 + s.L;
   }
@@ -185,25 +196,27 @@ MLA_DEV void run_start(const AttnArgs& a, int w, Cursor* cur) {
   if (w == 0 && bad) set_error(a.error, kErrSeqLen);
   const long long quota = max(1ll, (total + a.workers - 1) / a.workers);
   cur->quota = quota;
-  cur->u = min((long long)w * quota, total);
-  cur->end = min(cur->u + quota, total);
+  const long long u = min((long long)w * quota, total);
+  cur->item = u;
+  cur->end = min(u + quota, total);
   cur->s = Seq{0, 0, 0, 0};
   cur->b = cur->qb = cur->h = cur->t0 = 0;
-  cur->tiles = cur->group = 1;
-  if (!cur->more()) return;
+  cur->tiles = 0;
+  cur->group = 1;
+  if (u >= total) return;
   long long before = 0;
   for (int b0 = 0; b0 < a.batch; b0 += 32) {
     Seq s{0, 0, 0, 0};
     const int b = b0 + lane;
     if (b < a.batch) s.load(a, b);
-    const long long own = s.tiles_before(s.blocks(), a.causal) * a.heads;
+    const long long own = s.units_before(s.blocks(), a.causal) * a.heads;
     long long incl = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(~0u, incl, o);
       if (lane >= o) incl += y;
     }
-    const unsigned beyond = __ballot_sync(~0u, before + incl > cur->u);
+    const unsigned beyond = __ballot_sync(~0u, before + incl > u);
     if (beyond) {
       const int src = __ffs(beyond) - 1;
       cur->b = b0 + src;
@@ -212,27 +225,28 @@ MLA_DEV void run_start(const AttnArgs& a, int w, Cursor* cur) {
       cur->s.k0 = __shfl_sync(~0u, s.k0, src);
       cur->s.L = __shfl_sync(~0u, s.L, src);
       cur->group = Cursor::group_heads(a, cur->s, quota);
-      long long rest = cur->u - before - __shfl_sync(~0u, incl - own, src);
-      const long long per_head = cur->s.tiles_before(cur->s.blocks(), a.causal);
+      long long rest = u - before - __shfl_sync(~0u, incl - own, src);
+      const long long per_head = cur->s.units_before(cur->s.blocks(), a.causal);
       const int g0 = (int)(rest / (per_head * cur->group)) * cur->group;  // the group's first head
       const int heads = min(cur->group, a.heads - g0);
       rest -= per_head * g0;
       int lo = 0, hi = cur->s.blocks() - 1;  // the last block that starts at or before `rest`
       while (lo < hi) {
         const int mid = (lo + hi + 1) / 2;
-        if (cur->s.tiles_before(mid, a.causal) * heads <= rest) lo = mid;
+        if (cur->s.units_before(mid, a.causal) * heads <= rest) lo = mid;
         else hi = mid - 1;
       }
       cur->qb = lo;
       cur->tiles = cur->s.tiles((lo + 1) * kBlockQ, a.causal);
-      rest -= cur->s.tiles_before(lo, a.causal) * heads;
-      cur->h = g0 + (int)(rest / cur->tiles);
-      cur->t0 = (int)(rest % cur->tiles);
+      rest -= cur->s.units_before(lo, a.causal) * heads;
+      const int units = cur->tiles + kItemUnits, in_item = (int)(rest % units);
+      cur->h = g0 + (int)(rest / units);
+      cur->item = u - in_item;
+      cur->t0 = max(0, in_item - kItemUnits);
       return;
     }
     before += __shfl_sync(~0u, incl, 31);
   }
-  cur->end = cur->u;  // not reached: the units add up to the total
 }
 
 // An item whose rows a softmax warp has still to write.
@@ -574,7 +588,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
       const int t0 = more ? at.t0 : 0, t1 = more ? at.t1() : 0, r0 = at.qb * kBlockQ + kTile * rank;
       if (rank == 0 && threadIdx.x == 0 && more && t0 == 0 && t1 < at.tiles) {
         // the item goes on in the following runs
-        const long long last = (at.u + at.tiles - 1) / at.quota;
+        const long long last = (at.item + kItemUnits + at.tiles - 1) / at.quota;
         a.info[worker] = SplitInfo{(int)(last - worker) + 1, at.s.q0 + at.qb * kBlockQ,
                                    min(at.s.n - at.qb * kBlockQ, kBlockQ), at.h};
       }
@@ -723,51 +737,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
   if (warp == 8) tmem_dealloc_pair(tmem, kTmemAll);
 }
 
-// Merge of split items: block (w, g) joins 16 rows of the item that run w
-// starts and does not finish. Its parts are run w's second slot and the first
-// slots of the following runs; a thread holds 16 of a row's 128 columns.
-constexpr int kMergeRows = 16;
-__global__ void __launch_bounds__(128) mla_prefill_merge_kernel(const AttnArgs a) {
+// Merge of split items: block (w, g) joins 8 rows of the item that run w starts
+// and does not finish, a warp each, four columns to a lane. The parts are run w's
+// second slot and the first slots of the following runs; lane p holds the lse of
+// part p (of p + 32, ... in turn for a longer list).
+constexpr int kMergeRows = 8;
+__global__ void __launch_bounds__(32 * kMergeRows) mla_prefill_merge_kernel(const AttnArgs a) {
   grid_dependency_wait();
-  const int w = blockIdx.x;
+  const int w = blockIdx.x, lane = threadIdx.x & 31;
   const SplitInfo it = a.info[w];
-  const int row = blockIdx.y * kMergeRows + (threadIdx.x >> 3), col = (threadIdx.x & 7) * 16;
+  const int row = blockIdx.y * kMergeRows + (threadIdx.x >> 5);
   const int pieces = min(it.pieces, a.workers - w);
   if (pieces < 1 || row >= it.rows) return;
   const auto slot = [&](int p) { return (size_t)(p == 0 ? 2 * w + 1 : 2 * (w + p)) * kBlockQ + row; };
   float m = -INFINITY;
-  for (int p = 0; p < pieces; ++p) m = fmaxf(m, a.part_lse[slot(p)]);
-  float acc[16], sum = 0.f;
+  for (int p = lane; p < pieces; p += 32) m = fmaxf(m, a.part_lse[slot(p)]);
 #pragma unroll
-  for (int x = 0; x < 16; ++x) acc[x] = 0.f;
-  if (m != -INFINITY) {
-    for (int p = 0; p < pieces; ++p) {
-      const size_t at = slot(p);
-      const float lse = a.part_lse[at];
-      if (lse == -INFINITY) continue;
-      const float f = expf(lse - m);
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.f;
+  for (int p0 = 0; p0 < pieces; p0 += 32) {
+    const int mine = p0 + lane;
+    const float lse = mine < pieces ? a.part_lse[slot(mine)] : -INFINITY;
+    const float weight = lse == -INFINITY ? 0.f : expf(lse - m);
+    const int count = min(32, pieces - p0);
+#pragma unroll 4
+    for (int p = 0; p < count; ++p) {
+      const float f = __shfl_sync(~0u, weight, p);
+      const float4 v = reinterpret_cast<const float4*>(a.part_o + slot(p0 + p) * 128)[lane];
       sum += f;
-      const float4* src = reinterpret_cast<const float4*>(a.part_o + at * 128 + col);
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const float4 v = src[x];
-        acc[4 * x] += f * v.x;
-        acc[4 * x + 1] += f * v.y;
-        acc[4 * x + 2] += f * v.z;
-        acc[4 * x + 3] += f * v.w;
+      if (f > 0.f) {  // a part without keys counts for nothing, whatever its rows hold
+        acc.x = fmaf(f, v.x, acc.x);
+        acc.y = fmaf(f, v.y, acc.y);
+        acc.z = fmaf(f, v.z, acc.z);
+        acc.w = fmaf(f, v.w, acc.w);
       }
     }
   }
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
   const size_t r = (size_t)(it.row + row) * a.heads + it.head;
-  uint4* dst = reinterpret_cast<uint4*>(a.out + r * 128 + col);
-#pragma unroll
-  for (int x = 0; x < 2; ++x)
-    dst[x] = make_uint4(pack_bf16x2(acc[8 * x] * inv, acc[8 * x + 1] * inv),
-                        pack_bf16x2(acc[8 * x + 2] * inv, acc[8 * x + 3] * inv),
-                        pack_bf16x2(acc[8 * x + 4] * inv, acc[8 * x + 5] * inv),
-                        pack_bf16x2(acc[8 * x + 6] * inv, acc[8 * x + 7] * inv));
-  if (col == 0) a.lse[r] = sum > 0.f ? m + logf(sum) : -INFINITY;
+  reinterpret_cast<uint2*>(a.out + r * 128)[lane] =
+      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  if (lane == 0) a.lse[r] = sum > 0.f ? m + logf(sum) : -INFINITY;
 }
 
 mla_status_t check_attention(const mlap_attention_desc_t* d) {
@@ -864,7 +875,7 @@ mla_status_t attention(const mlap_attention_desc_t* d, const void* q, const void
   if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(workers, kBlockQ / kMergeRows, 1);
-  cfg.blockDim = dim3(128, 1, 1);
+  cfg.blockDim = dim3(32 * kMergeRows, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
