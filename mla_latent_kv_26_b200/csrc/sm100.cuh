@@ -140,8 +140,15 @@ MLA_DEV void tma_load_3d(uint32_t dst, const CUtensorMap* map, int32_t c0, int32
       : "memory");
 }
 
-// The same, into this CTA's shared memory, completing the bytes on a barrier
-// of either CTA of the pair (a shared::cluster address).
+// The same (2-D, 3-D), into this CTA's shared memory, completing the bytes on a
+// barrier of either CTA of the pair (a shared::cluster address).
+MLA_DEV void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, int32_t c0, int32_t c1, uint32_t cluster_bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+      "%3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(c0), "r"(c1), "r"(cluster_bar)
+      : "memory");
+}
 MLA_DEV void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map, int32_t c0, int32_t c1, int32_t c2,
                               uint32_t cluster_bar) {
   asm volatile(
@@ -168,6 +175,18 @@ MLA_DEV void tma_store_2d(const CUtensorMap* map, uint32_t src, int32_t c0, int3
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(c0),
                "r"(c1), "r"(src)
                : "memory");
+}
+// L2 cache policies, and the store with one.
+MLA_DEV uint64_t l2_evict_first() {
+  uint64_t policy;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+  return policy;
+}
+MLA_DEV void tma_store_2d_hint(const CUtensorMap* map, uint32_t src, int32_t c0, int32_t c1, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group.L2::cache_hint [%0, {%1, %2}], [%3], %4;" ::"l"(map),
+      "r"(c0), "r"(c1), "r"(src), "l"(policy)
+      : "memory");
 }
 MLA_DEV void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 MLA_DEV void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
