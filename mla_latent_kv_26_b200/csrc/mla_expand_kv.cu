@@ -23,6 +23,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
+#include <mutex>
 
 #include "mla.h"
 #include "mla_prefill.h"
@@ -230,6 +231,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads, 1)
   if (warp == 4) tmem_dealloc_pair(tmem, 512);
 }
 
+// SMs of the current device, the kernel's shared memory opted into (once per
+// device); 0 on a CUDA error.
+int expand_sms() {
+  static std::mutex mu;
+  static int sms[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+    cudaGetLastError();
+    return 0;
+  }
+  std::lock_guard<std::mutex> lock(mu);
+  if (sms[dev] == 0) {
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        cudaFuncSetAttribute((const void*)mla_expand_kv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kExpSmem) != cudaSuccess) {
+      cudaGetLastError();
+      return 0;
+    }
+    sms[dev] = n;
+  }
+  return sms[dev];
+}
+
 mla_status_t expand(const mlap_expand_desc_t* d, const void* rows, const void* wkv_b, const int32_t* row_count,
                     void* kv, uint32_t* error, cudaStream_t stream) {
   if (!d) return MLA_ERR_INVALID_ARG;
@@ -241,12 +266,8 @@ mla_status_t expand(const mlap_expand_desc_t* d, const void* rows, const void* w
   if (!rows || !wkv_b || !kv) return MLA_ERR_INVALID_ARG;
   const auto off = [](const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) != 0; };
   if (off(rows, 16) || off(wkv_b, 16) || off(kv, 16) || off(row_count, 4) || off(error, 4)) return MLA_ERR_INVALID_ARG;
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-    cudaGetLastError();
-    return MLA_ERR_CUDA;
-  }
+  const int sms = expand_sms();
+  if (sms == 0) return MLA_ERR_CUDA;
   PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
   if (!enc) return MLA_ERR_CUDA;
   const auto encode = [&](CUtensorMap* m, const void* p, long long cols, long long n, long long stride, int box_rows) {
@@ -260,9 +281,6 @@ mla_status_t expand(const mlap_expand_desc_t* d, const void* rows, const void* w
   const long long width = (long long)d->num_heads * 256;
   if (!encode(&maps.rows, rows, kDLatent, d->num_rows, d->row_stride, 128) ||
       !encode(&maps.w, wkv_b, kDLatent, width, kDLatent, 128) || !encode(&maps.kv, kv, width, d->num_rows, width, 32))
-    return MLA_ERR_CUDA;
-  if (cudaFuncSetAttribute((const void*)mla_expand_kv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kExpSmem) !=
-      cudaSuccess)
     return MLA_ERR_CUDA;
   ExpandArgs a{row_count, static_cast<__nv_bfloat16*>(kv), error, d->num_rows, d->num_heads};
   const long long tiles = (long long)((d->num_rows + kExpRows - 1) / kExpRows) * d->num_heads;

@@ -48,6 +48,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 #include <math.h>
+#include <mutex>
 
 #include "mla.h"
 #include "mla_prefill.h"
@@ -793,14 +794,34 @@ mla_status_t check_attention(const mlap_attention_desc_t* d) {
   return MLA_OK;
 }
 
-// Workers (CTA pairs) of the current device for this descriptor; 0 on a CUDA error.
-int attention_workers(const mlap_attention_desc_t* d) {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+// SMs of the current device, the kernel's shared memory opted into (once per
+// device); 0 on a CUDA error.
+int device_sms() {
+  static std::mutex mu;
+  static int sms[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
     cudaGetLastError();
     return 0;
   }
+  std::lock_guard<std::mutex> lock(mu);
+  if (sms[dev] == 0) {
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        cudaFuncSetAttribute((const void*)mla_prefill_attention_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kAttnSmem) != cudaSuccess) {
+      cudaGetLastError();
+      return 0;
+    }
+    sms[dev] = n;
+  }
+  return sms[dev];
+}
+
+// Workers (CTA pairs) of the current device for this descriptor; 0 on a CUDA error.
+int attention_workers(const mlap_attention_desc_t* d) {
+  int sms = device_sms();
+  if (sms == 0) return 0;
   if (d->num_sms > 0 && d->num_sms < sms) sms = d->num_sms;
   return sms < 2 ? 1 : sms / 2;
 }
@@ -868,9 +889,6 @@ mla_status_t attention(const mlap_attention_desc_t* d, const void* q, const void
   a.workers = workers;
   a.scale = d->softmax_scale;
   a.scale_log2 = d->softmax_scale * 1.4426950408889634f;
-  if (cudaFuncSetAttribute((const void*)mla_prefill_attention_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           kAttnSmem) != cudaSuccess)
-    return MLA_ERR_CUDA;
   mla_prefill_attention_kernel<<<2 * workers, kAttnThreads, kAttnSmem, stream>>>(maps, a);
   if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};

@@ -20,49 +20,89 @@ a causal descriptor does less work.
 
 from __future__ import annotations
 
+import contextlib
 from typing import Optional, Tuple
 
 import torch
 
 from . import binding as B
 
+_BF16, _I32, _U8, _F32 = torch.bfloat16, torch.int32, torch.uint8, torch.float32
+_HERE = contextlib.nullcontext()
+
 
 def _check(name, t, dtype, shape, dev):
-    if not isinstance(t, torch.Tensor) or t.device != dev or t.dtype != dtype or not t.is_contiguous():
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != dev or not t.is_contiguous():
         raise ValueError(f"{name}: need a contiguous {dtype} tensor on {dev}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
 
 
 def _device(name, t):
-    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name}: need a CUDA tensor")
     return t.device
 
 
 def _row_stride(name, t, dev, width, exact):
     """Elements between the rows of a bf16 matrix whose rows are dense."""
-    if t.device != dev or t.dtype != torch.bfloat16 or t.dim() != 2:
+    if not isinstance(t, torch.Tensor) or t.device != dev or t.dtype != _BF16 or t.dim() != 2:
         raise ValueError(f"{name}: need a two-dimensional bfloat16 tensor on {dev}")
-    if t.shape[1] != width if exact else t.shape[1] < width:
-        raise ValueError(f"{name}: rows of {t.shape[1]} values, {'' if exact else 'at least '}{width} needed")
-    if t.shape[0] <= 1:
-        stride = (t.shape[1] + 7) // 8 * 8  # the stride of a single row is never used
-    else:
-        stride = t.stride(0)
-    if (t.numel() and t.stride(1) != 1) or stride < width or stride % 8 or t.data_ptr() % 16:
+    rows, cols = t.shape
+    if cols != width if exact else cols < width:
+        raise ValueError(f"{name}: rows of {cols} values, {'' if exact else 'at least '}{width} needed")
+    s0, s1 = t.stride()
+    stride = s0 if rows > 1 else (cols + 7) // 8 * 8  # the stride of a single row is never used
+    if (rows and s1 != 1) or stride < width or stride % 8 or t.data_ptr() % 16:
         raise ValueError(f"{name}: rows must be dense, 16-byte aligned and a multiple of 8 elements apart")
     return stride
 
 
-def _error_word(error_word, dev):
-    if error_word is not None and (error_word.device != dev or error_word.dtype != torch.int32
-                                   or error_word.numel() < 1):
-        raise ValueError(f"error_word: need an int32 tensor on {dev}")
+def _optional_i32(name, t, dev):
+    if t is not None and (not isinstance(t, torch.Tensor) or t.device != dev or t.dtype != _I32 or t.numel() < 1):
+        raise ValueError(f"{name}: need an int32 tensor on {dev}")
+
+
+def _on(dev):
+    """The device as a context; nothing when it is the current one."""
+    return _HERE if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
 
 
 def _stream(stream, dev):
-    return torch.cuda.current_stream(dev) if stream is None else stream
+    # the raw handle: making a torch.cuda.Stream object takes longer than a launch
+    return torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream
+
+
+def _check_cache(kv_cache, block_table, row_offsets, starts, dev):
+    """(fp8, batch) of a paged cache and its tables."""
+    if not isinstance(kv_cache, torch.Tensor) or not isinstance(block_table, torch.Tensor):
+        raise ValueError("kv_cache, block_table: need tensors")
+    fp8 = kv_cache.dtype == _U8
+    if kv_cache.dim() != 3 or kv_cache.shape[1:] != (64, 656 if fp8 else 576) or block_table.dim() != 2:
+        raise ValueError("kv_cache must be [pages, 64, 576] bf16 or [pages, 64, 656] uint8, "
+                         "block_table [batch, max_pages_per_seq]")
+    batch, width = block_table.shape
+    if kv_cache.shape[0] == 0 or width == 0:
+        raise ValueError("kv_cache, block_table: empty")
+    _check("kv_cache", kv_cache, _U8 if fp8 else _BF16, None, dev)
+    _check("block_table", block_table, _I32, None, dev)
+    _check("row_offsets", row_offsets, _I32, (batch + 1,), dev)
+    if starts is not None:
+        _check("starts", starts, _I32, (batch,), dev)
+    return fp8, batch
+
+
+def _launch_read(fp8, kv_cache, block_table, row_offsets, starts, out, error_word, stream):
+    desc = B.mlap_read_desc_t(block_table.shape[0], block_table.shape[1], kv_cache.shape[0], out.shape[0], 512, 64, 64)
+    fn = B.mlap_cache_read_fp8 if fp8 else B.mlap_cache_read
+    B.check(fn(desc, kv_cache, block_table, row_offsets, starts, out, error_word, stream), "mlap_cache_read")
+
+
+def _check_wkv_b(wkv_b, dev):
+    if not isinstance(wkv_b, torch.Tensor) or wkv_b.dim() != 3:
+        raise ValueError("wkv_b: need a [heads, 256, 512] tensor")
+    _check("wkv_b", wkv_b, _BF16, (wkv_b.shape[0], 256, 512), dev)
+    return wkv_b.shape[0]
 
 
 def cache_read(kv_cache: torch.Tensor, block_table: torch.Tensor, row_offsets: torch.Tensor, *,
@@ -78,30 +118,17 @@ def cache_read(kv_cache: torch.Tensor, block_table: torch.Tensor, row_offsets: t
     allocate. Rows that no sequence owns are left as they were; a position
     without a page gives a row of zeros and a bit in ``error_word``."""
     dev = _device("kv_cache", kv_cache)
-    fp8 = kv_cache.dtype == torch.uint8
-    _check("kv_cache", kv_cache, torch.uint8 if fp8 else torch.bfloat16, None, dev)
-    _check("block_table", block_table, torch.int32, None, dev)
-    if kv_cache.dim() != 3 or tuple(kv_cache.shape[1:]) != (64, 656 if fp8 else 576) or block_table.dim() != 2:
-        raise ValueError("kv_cache must be [pages, 64, 576] bf16 or [pages, 64, 656] uint8, "
-                         "block_table [batch, max_pages_per_seq]")
-    batch = block_table.shape[0]
-    _check("row_offsets", row_offsets, torch.int32, (batch + 1,), dev)
-    if starts is not None:
-        _check("starts", starts, torch.int32, (batch,), dev)
-    _error_word(error_word, dev)
+    fp8, _ = _check_cache(kv_cache, block_table, row_offsets, starts, dev)
+    _optional_i32("error_word", error_word, dev)
     if out is None:
         if num_rows is None:
             raise ValueError("cache_read needs out or num_rows")
-        out = torch.empty(num_rows, 576, dtype=torch.bfloat16, device=dev)
-    _check("out", out, torch.bfloat16, (out.shape[0], 576), dev)
-    desc = B.make_read_desc(batch=batch, max_pages_per_seq=max(block_table.shape[1], 1),
-                            num_pages=max(kv_cache.shape[0], 1), num_rows=out.shape[0])
-    if batch and out.shape[0] and (kv_cache.shape[0] == 0 or block_table.shape[1] == 0):
-        raise ValueError("cache_read: rows asked of an empty cache or block table")
-    with torch.cuda.device(dev):
-        fn = B.mlap_cache_read_fp8 if fp8 else B.mlap_cache_read
-        B.check(fn(desc, kv_cache, block_table, row_offsets, starts, out, error_word, _stream(stream, dev)),
-                "mlap_cache_read")
+        out = torch.empty(num_rows, 576, dtype=_BF16, device=dev)
+    elif out.dim() != 2:
+        raise ValueError("out: need a [rows, 576] tensor")
+    _check("out", out, _BF16, (out.shape[0], 576), dev)
+    with _on(dev):
+        _launch_read(fp8, kv_cache, block_table, row_offsets, starts, out, error_word, _stream(stream, dev))
     return out
 
 
@@ -115,20 +142,15 @@ def expand_kv(rows: torch.Tensor, wkv_b: torch.Tensor, *, out: Optional[torch.Te
     nor written."""
     dev = _device("rows", rows)
     stride = _row_stride("rows", rows, dev, 512, False)
-    M = rows.shape[0]
-    if not isinstance(wkv_b, torch.Tensor) or wkv_b.dim() != 3:
-        raise ValueError("wkv_b: need a [heads, 256, 512] tensor")
-    H = wkv_b.shape[0]
-    _check("wkv_b", wkv_b, torch.bfloat16, (H, 256, 512), dev)
-    if row_count is not None and (row_count.device != dev or row_count.dtype != torch.int32 or row_count.numel() < 1):
-        raise ValueError(f"row_count: need an int32 tensor on {dev}")
-    _error_word(error_word, dev)
+    M, H = rows.shape[0], _check_wkv_b(wkv_b, dev)
+    _optional_i32("row_count", row_count, dev)
+    _optional_i32("error_word", error_word, dev)
     if out is None:
-        out = torch.empty(M, H, 256, dtype=torch.bfloat16, device=dev)
-    _check("out", out, torch.bfloat16, (M, H, 256), dev)
-    with torch.cuda.device(dev):
-        B.check(B.mlap_expand_kv(B.make_expand_desc(num_rows=M, num_heads=H, row_stride=stride), rows, wkv_b,
-                                 row_count, out, error_word, _stream(stream, dev)), "mlap_expand_kv")
+        out = torch.empty(M, H, 256, dtype=_BF16, device=dev)
+    _check("out", out, _BF16, (M, H, 256), dev)
+    with _on(dev):
+        B.check(B.mlap_expand_kv(B.mlap_expand_desc_t(M, H, stride, 128, 512, 128), rows, wkv_b, row_count, out,
+                                 error_word, _stream(stream, dev)), "mlap_expand_kv")
     return out
 
 
@@ -161,34 +183,35 @@ def prefill_attention(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, cu_
     if q.dim() != 3:
         raise ValueError("q: need a [queries, heads, 192] tensor")
     Nq, H = q.shape[0], q.shape[1]
-    _check("q", q, torch.bfloat16, (Nq, H, 192), dev)
+    _check("q", q, _BF16, (Nq, H, 192), dev)
+    if not isinstance(kv, torch.Tensor) or kv.dim() != 3:
+        raise ValueError("kv: need a [keys, heads, 256] tensor")
     Nk = kv.shape[0]
-    _check("kv", kv, torch.bfloat16, (Nk, H, 256), dev)
+    _check("kv", kv, _BF16, (Nk, H, 256), dev)
     stride = _row_stride("k_pe", k_pe, dev, 64, True)
     if k_pe.shape[0] != Nk:
         raise ValueError(f"k_pe: {k_pe.shape[0]} rows, kv has {Nk}")
+    _check("cu_q", cu_q, _I32, None, dev)
     if cu_q.dim() != 1 or cu_q.shape[0] < 1:
         raise ValueError("cu_q: need batch + 1 offsets")
-    _check("cu_q", cu_q, torch.int32, None, dev)
-    _check("cu_k", cu_k, torch.int32, tuple(cu_q.shape), dev)
-    _error_word(error_word, dev)
+    _check("cu_k", cu_k, _I32, cu_q.shape, dev)
+    _optional_i32("error_word", error_word, dev)
     if out is None:
-        out = torch.empty(Nq, H, 128, dtype=torch.bfloat16, device=dev)
+        out = torch.empty(Nq, H, 128, dtype=_BF16, device=dev)
     if lse is None:
-        lse = torch.empty(Nq, H, dtype=torch.float32, device=dev)
-    _check("out", out, torch.bfloat16, (Nq, H, 128), dev)
-    _check("lse", lse, torch.float32, (Nq, H), dev)
-    desc = B.make_attention_desc(batch=cu_q.shape[0] - 1, num_heads=H, num_q=Nq, num_k=Nk, pe_stride=stride,
-                                 causal=causal, softmax_scale=softmax_scale, num_sms=num_sms)
-    s = _stream(stream, dev)
-    with torch.cuda.device(dev):
+        lse = torch.empty(Nq, H, dtype=_F32, device=dev)
+    _check("out", out, _BF16, (Nq, H, 128), dev)
+    _check("lse", lse, _F32, (Nq, H), dev)
+    desc = B.mlap_attention_desc_t(cu_q.shape[0] - 1, H, Nq, Nk, stride, int(bool(causal)), softmax_scale, num_sms,
+                                   128, 64, 128)
+    with _on(dev):
         if workspace is None:
-            n = max(B.mlap_attention_workspace_bytes(desc), 16)
-            with torch.cuda.stream(s):
-                workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-        _check("workspace", workspace, torch.uint8, None, dev)
-        B.check(B.mlap_attention(desc, q, kv, k_pe, cu_q, cu_k, out, lse, workspace, workspace.numel(), error_word, s),
-                "mlap_attention")
+            n = max(B.mlap_attention_workspace_bytes(desc), 32)
+            with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+                workspace = torch.empty(n, dtype=_U8, device=dev)
+        _check("workspace", workspace, _U8, None, dev)
+        B.check(B.mlap_attention(desc, q, kv, k_pe, cu_q, cu_k, out, lse, workspace, workspace.numel(), error_word,
+                                 _stream(stream, dev)), "mlap_attention")
     return out, lse
 
 
@@ -230,6 +253,7 @@ class MlaPrefill:
         self.out = torch.empty(max_queries, num_heads, 128, dtype=torch.bfloat16, device=dev)
         self.lse = torch.empty(max_queries, num_heads, dtype=torch.float32, device=dev)
         self.error_word = torch.zeros(1, dtype=torch.int32, device=dev)
+        self._expand_desc = B.make_expand_desc(num_rows=max_keys, num_heads=num_heads)
 
     def __call__(self, q: torch.Tensor, wkv_b: torch.Tensor, kv_cache: torch.Tensor, block_table: torch.Tensor,
                  cu_q: torch.Tensor, cu_k: torch.Tensor, *, starts: Optional[torch.Tensor] = None,
@@ -238,14 +262,23 @@ class MlaPrefill:
         its cached positions ``starts[b] .. starts[b] + cu_k[b + 1] - cu_k[b] - 1``
         (``starts`` None: from 0). Returns ``out`` [Nq, H, 128], a view of a
         buffer that the next call overwrites; its log-sum-exp is ``self.lse[:Nq]``."""
-        nq = q.shape[0]
-        if nq > self.out.shape[0] or q.dim() != 3 or q.shape[1] != self.num_heads:
-            raise ValueError(f"q: shape {tuple(q.shape)}, need at most {self.out.shape[0]} queries of "
-                             f"{self.num_heads} heads")
-        e = self.error_word
-        cache_read(kv_cache, block_table, cu_k, starts=starts, out=self.rows, error_word=e, stream=stream)
-        expand_kv(self.rows, wkv_b, out=self.kv, row_count=cu_k[-1:], error_word=e, stream=stream)
-        out, _ = prefill_attention(q, self.kv, self.rows[:, 512:], cu_q, cu_k, causal=causal,
-                                   softmax_scale=self.softmax_scale, out=self.out[:nq], lse=self.lse[:nq],
-                                   workspace=self.workspace, num_sms=self.num_sms, error_word=e, stream=stream)
+        dev = self.device
+        if not isinstance(q, torch.Tensor) or q.dim() != 3 or q.shape[0] > self.out.shape[0]:
+            raise ValueError(f"q: need a [queries, {self.num_heads}, 192] tensor of at most {self.out.shape[0]} queries")
+        nq, H, M = q.shape[0], self.num_heads, self.rows.shape[0]
+        _check("q", q, _BF16, (nq, H, 192), dev)
+        if _check_wkv_b(wkv_b, dev) != H:
+            raise ValueError(f"wkv_b: {wkv_b.shape[0]} heads, {H} needed")
+        fp8, batch = _check_cache(kv_cache, block_table, cu_k, starts, dev)
+        _check("cu_q", cu_q, _I32, (batch + 1,), dev)
+        out, e = self.out[:nq], self.error_word
+        with _on(dev):
+            s = _stream(stream, dev)
+            _launch_read(fp8, kv_cache, block_table, cu_k, starts, self.rows, e, s)
+            B.check(B.mlap_expand_kv(self._expand_desc, self.rows, wkv_b, cu_k.data_ptr() + 4 * batch, self.kv, e, s),
+                    "mlap_expand_kv")
+            desc = B.mlap_attention_desc_t(batch, H, nq, M, 576, int(bool(causal)), self.softmax_scale, self.num_sms,
+                                           128, 64, 128)
+            B.check(B.mlap_attention(desc, q, self.kv, self.rows.data_ptr() + 1024, cu_q, cu_k, out, self.lse,
+                                     self.workspace, self.workspace.numel(), e, s), "mlap_attention")
         return out
