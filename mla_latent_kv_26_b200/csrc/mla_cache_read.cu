@@ -59,6 +59,8 @@ template <bool kF8>
 __global__ void __launch_bounds__(kReadWarps * 32) mla_cache_read_kernel(const ReadArgs a) {
   const int lane = threadIdx.x & 31;
   const int row0 = (int)(blockIdx.x * kReadWarps + (threadIdx.x >> 5)) * kRowsPerWarp;
+  allow_dependents();
+  grid_dependency_wait();
   const int end = __ldg(a.offsets + a.batch);
   uint32_t err = 0u;
   if (blockIdx.x == 0) {  // the first block reports offsets out of range or out of order
@@ -145,9 +147,10 @@ mla_status_t cache_read(const mlap_read_desc_t* d, const void* cache, const int3
              d->batch, d->max_pages_per_seq, d->num_pages, d->num_rows};
   const int per = kReadWarps * kRowsPerWarp;
   const int grid = (d->num_rows + per - 1) / per;
-  if (fp8) mla_cache_read_kernel<true><<<grid, kReadWarps * 32, 0, stream>>>(a);
-  else mla_cache_read_kernel<false><<<grid, kReadWarps * 32, 0, stream>>>(a);
-  return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+  return launch_dependent(fp8 ? mla_cache_read_kernel<true> : mla_cache_read_kernel<false>, dim3(grid), kReadWarps * 32, 0,
+                          stream, a) == cudaSuccess
+             ? MLA_OK
+             : MLA_ERR_CUDA;
 }
 
 }  // namespace prefill

@@ -77,6 +77,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_ctarank();
   Waiter W{&sh.abort_flag, a.error};
+  allow_dependents();
+  grid_dependency_wait();
   const int rows = a.row_count ? min(max(__ldg(a.row_count), 0), a.num_rows) : a.num_rows;
   const long long tiles = (long long)((rows + kExpRows - 1) / kExpRows) * a.heads;
   const int pairs = gridDim.x / 2;
@@ -285,8 +287,9 @@ mla_status_t expand(const mlap_expand_desc_t* d, const void* rows, const void* w
   ExpandArgs a{row_count, static_cast<__nv_bfloat16*>(kv), error, d->num_rows, d->num_heads};
   const long long tiles = (long long)((d->num_rows + kExpRows - 1) / kExpRows) * d->num_heads;
   const int pairs = (int)(tiles < sms / 2 ? tiles : (sms < 2 ? 1 : sms / 2));
-  mla_expand_kv_kernel<<<2 * pairs, kExpThreads, kExpSmem, stream>>>(maps, a);
-  return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+  return launch_dependent(mla_expand_kv_kernel, dim3(2 * pairs), kExpThreads, kExpSmem, stream, maps, a) == cudaSuccess
+             ? MLA_OK
+             : MLA_ERR_CUDA;
 }
 
 }  // namespace prefill

@@ -152,7 +152,7 @@ struct Cursor {
   // Heads of a group: about a run's number of items of this sequence.
   MLA_DEV static int group_heads(const AttnArgs& a, const Seq& s, long long quota) {
     const long long per_head = s.units_before(s.blocks(), a.causal);
-    return (int)min((long long)a.heads, max(1ll, (quota * s.blocks() + per_head / 2) / max(per_head, 1ll)));
+    return (int)min((long long)a.heads, max(1ll, quotient(quota * s.blocks() + per_head / 2, max(per_head, 1ll))));
   }
   MLA_DEV void next(const AttnArgs& a) {
     item += kItemUnits + tiles;
@@ -195,7 +195,7 @@ MLA_DEV void run_start(const AttnArgs& a, int w, Cursor* cur) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(~0u, total, o);
   if (w == 0 && bad) set_error(a.error, kErrSeqLen);
-  const long long quota = max(1ll, (total + a.workers - 1) / a.workers);
+  const long long quota = max(1ll, quotient(total + a.workers - 1, a.workers));
   cur->quota = quota;
   const long long u = min((long long)w * quota, total);
   cur->item = u;
@@ -228,7 +228,7 @@ MLA_DEV void run_start(const AttnArgs& a, int w, Cursor* cur) {
       cur->group = Cursor::group_heads(a, cur->s, quota);
       long long rest = u - before - __shfl_sync(~0u, incl - own, src);
       const long long per_head = cur->s.units_before(cur->s.blocks(), a.causal);
-      const int g0 = (int)(rest / (per_head * cur->group)) * cur->group;  // the group's first head
+      const int g0 = (int)quotient(rest, per_head * cur->group) * cur->group;  // the group's first head
       const int heads = min(cur->group, a.heads - g0);
       rest -= per_head * g0;
       int lo = 0, hi = cur->s.blocks() - 1;  // the last block that starts at or before `rest`
@@ -240,8 +240,9 @@ MLA_DEV void run_start(const AttnArgs& a, int w, Cursor* cur) {
       cur->qb = lo;
       cur->tiles = cur->s.tiles((lo + 1) * kBlockQ, a.causal);
       rest -= cur->s.units_before(lo, a.causal) * heads;
-      const int units = cur->tiles + kItemUnits, in_item = (int)(rest % units);
-      cur->h = g0 + (int)(rest / units);
+      const int units = cur->tiles + kItemUnits, items = (int)quotient(rest, units);
+      const int in_item = (int)(rest - (long long)items * units);
+      cur->h = g0 + items;
       cur->item = u - in_item;
       cur->t0 = max(0, in_item - kItemUnits);
       return;
@@ -345,7 +346,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     mbar_init(smem_addr(&sh.done), 2);         // the two issuers
     sh.abort_flag = 0u;
     fence_mbar_init();
-    if (rank == 0) a.info[worker].pieces = 0;
   }
   if (warp == 8) {
     tmem_alloc_pair(smem_addr(&sh.tmem), kTmemAll);
@@ -353,9 +353,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
   }
   if (warp == 9) {
     Cursor c;
+    grid_dependency_wait();
     run_start(a, worker, &c);
     if (lane == 0) {
       sh.start = c;
+      if (rank == 0) a.info[worker].pieces = 0;
       prefetch_tmap(&maps.q);
       prefetch_tmap(&maps.k);
       prefetch_tmap(&maps.v);
@@ -365,6 +367,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
+  grid_dependency_wait();  // every thread, for its own accesses
   const uint32_t tmem = sh.tmem;
   Cursor cur = sh.start;
   // an entry of the even CTA's barriers, for both CTAs
@@ -589,7 +592,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
       const int t0 = more ? at.t0 : 0, t1 = more ? at.t1() : 0, r0 = at.qb * kBlockQ + kTile * rank;
       if (rank == 0 && threadIdx.x == 0 && more && t0 == 0 && t1 < at.tiles) {
         // the item goes on in the following runs
-        const long long last = (at.item + kItemUnits + at.tiles - 1) / at.quota;
+        const long long last = quotient(at.item + kItemUnits + at.tiles - 1, at.quota);
         a.info[worker] = SplitInfo{(int)(last - worker) + 1, at.s.q0 + at.qb * kBlockQ,
                                    min(at.s.n - at.qb * kBlockQ, kBlockQ), at.h};
       }
@@ -889,18 +892,13 @@ mla_status_t attention(const mlap_attention_desc_t* d, const void* q, const void
   a.workers = workers;
   a.scale = d->softmax_scale;
   a.scale_log2 = d->softmax_scale * 1.4426950408889634f;
-  mla_prefill_attention_kernel<<<2 * workers, kAttnThreads, kAttnSmem, stream>>>(maps, a);
-  if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(workers, kBlockQ / kMergeRows, 1);
-  cfg.blockDim = dim3(32 * kMergeRows, 1, 1);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, mla_prefill_merge_kernel, a) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+  if (launch_dependent(mla_prefill_attention_kernel, dim3(2 * workers), kAttnThreads, kAttnSmem, stream, maps, a) !=
+      cudaSuccess)
+    return MLA_ERR_CUDA;
+  return launch_dependent(mla_prefill_merge_kernel, dim3(workers, kBlockQ / kMergeRows), 32 * kMergeRows, 0, stream, a) ==
+                 cudaSuccess
+             ? MLA_OK
+             : MLA_ERR_CUDA;
 }
 
 }  // namespace prefill

@@ -2,6 +2,7 @@
 // error bits they report.
 #pragma once
 
+#include <cuda_runtime.h>
 #include <stdint.h>
 
 #include "common.cuh"
@@ -55,6 +56,13 @@ struct Waiter {
   MLA_DEV bool wait_warp(uint64_t* bar, uint32_t parity) { return __all_sync(~0u, wait(bar, parity)); }
 };
 
+// a / b for a >= 0, b > 0; 32-bit where both fit (a 64-bit division takes
+// hundreds of cycles).
+MLA_DEV long long quotient(long long a, long long b) {
+  if (((unsigned long long)a | (unsigned long long)b) >> 32 == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
+
 // Range [*first, *first + return) of sequence b in ragged rows [0, rows):
 // offsets outside [0, rows] or out of order are clipped into it, so that no
 // caller's offsets make an access leave the rows.
@@ -63,6 +71,25 @@ MLA_DEV int ragged_range(const int32_t* offsets, int b, int rows, int* first) {
   const int a0 = min(max(o0, 0), rows);
   *first = a0;
   return min(max(o1, a0), rows) - a0;
+}
+
+// Launch with programmatic stream serialization: the kernel may be set up while
+// the one before it in the stream still runs, and reads and writes global memory
+// only behind grid_dependency_wait().
+template <typename Kernel, typename... Args>
+inline cudaError_t launch_dependent(Kernel kernel, dim3 grid, int threads, int smem, cudaStream_t stream,
+                                    const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 }  // namespace prefill
