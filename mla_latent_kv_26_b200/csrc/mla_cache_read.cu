@@ -11,7 +11,9 @@
 // Bound by HBM: 1152 (bf16) or 644 of 656 (fp8) bytes read and 1152 written
 // per row. One warp handles four output rows: 4 x 72 sixteen-byte pieces are
 // nine per lane, so that every lane has nine loads in flight and the warp's
-// stores are one contiguous run of 4608 bytes.
+// stores are one contiguous run of 4608 bytes. Blocks of four warps: 270k fp8
+// rows take 80 us (0.89 of the copy bandwidth), with eight 84 us, with eight
+// rows to a warp 89 us.
 #include <cuda_runtime.h>
 
 #include "mla.h"
@@ -31,7 +33,7 @@ struct ReadArgs {
   int batch, max_pages_per_seq, num_pages, num_rows;
 };
 
-constexpr int kReadWarps = 8;
+constexpr int kReadWarps = 4;
 constexpr int kRowsPerWarp = 4;
 constexpr int kRowBytes = kDQK * 2;
 constexpr int kPieces = kRowBytes / 16;                        // 72 per row
