@@ -113,7 +113,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads, 1)
   const auto m_tile = [&](long long i) { return (int)(i / a.heads); };
 
   if (warp == 5) {
-    if (lane == 0) {
+    if (elect_one()) {
       int n = 0, na = 0;  // weight blocks, sets of latents
       bool ok = true;
       for (long long i = i0; i < i1 && ok; ++i) {
@@ -143,7 +143,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads, 1)
     }
     __syncwarp();
   } else if (warp == 4) {
-    if (rank == 0 && lane == 0) {
+    if (rank == 0 && elect_one()) {
       constexpr uint32_t idesc = idesc_bf16_f32(256, 256, 0, 0);
       int n = 0, nt = 0, na = 0;
       bool ok = true;

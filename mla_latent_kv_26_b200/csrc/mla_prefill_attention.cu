@@ -185,6 +185,7 @@ MLA_DEV void run_start(const AttnArgs& a, int w, Cursor* cur) {
   const int lane = threadIdx.x & 31;
   long long total = 0;
   bool bad = false;
+#pragma unroll 1
   for (int b = lane; b < a.batch; b += 32) {
     Seq s;
     s.load(a, b);
@@ -206,6 +207,7 @@ MLA_DEV void run_start(const AttnArgs& a, int w, Cursor* cur) {
   cur->group = 1;
   if (u >= total) return;
   long long before = 0;
+#pragma unroll 1
   for (int b0 = 0; b0 < a.batch; b0 += 32) {
     Seq s{0, 0, 0, 0};
     const int b = b0 + lane;
@@ -379,7 +381,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
   }
   if (warp == 9) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
+    if (elect_one()) {
       Cursor ahead = cur;  // position of Q and K, three tiles before V
       RingPos pk, pv;
       int nq = 0, jk = ahead.t0;
@@ -407,9 +409,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
         }
         return true;
       };
+#pragma unroll 1
       for (int x = 0; x < kStages && ok; ++x) ok = load_k();
+#pragma unroll 1
       for (; cur.more() && ok; cur.next(a)) {
         const int t1 = cur.t1();
+#pragma unroll 1
         for (int j = cur.t0; j < t1; ++j, pv.next()) {
           if (!(ok = W.wait(&sh.pv_done[pv.s], pv.phase ^ 1))) break;  // V of three tiles ago is done with
           const uint32_t vs = stages + pv.s * kStageBytes + kKBytes;
@@ -436,15 +441,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     __syncwarp();
   } else if (warp == 8) {
     // ------------------------------------------------------------ MMA issuer: scores
-    if (rank == 0 && lane == 0) {
+    if (rank == 0 && elect_one()) {
       constexpr uint32_t idesc = idesc_bf16_f32(256, 128, 0, 0);
       RingPos p;
       int nq = 0, i = 0;  // query blocks, tiles
       bool ok = true;
+#pragma unroll 1
       for (; cur.more() && ok; cur.next(a), ++nq) {
         const int t1 = cur.t1(), b = nq & 1;
         if (!W.wait(&sh.q_full[b], (nq >> 1) & 1)) break;
         const uint64_t qd = smem_desc_sw128(qbuf + b * kQBytes, 16, 1024);
+#pragma unroll 1
         for (int j = cur.t0; j < t1; ++j, p.next(), ++i) {
           if (!(ok = W.wait(&sh.k_full[p.s], p.phase))) break;
           if (!(ok = W.wait(&sh.s_free[i & 1], ((i >> 1) & 1) ^ 1))) break;
@@ -467,14 +474,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     __syncwarp();
   } else if (warp == 11) {
     // ------------------------------------------------------------ MMA issuer: values
-    if (rank == 0 && lane == 0) {
+    if (rank == 0 && elect_one()) {
       constexpr uint32_t idesc = idesc_bf16_f32(256, 128, 0, 1);
       RingPos p;
       int no = 0, i = 0;  // items, tiles
       bool ok = true;
+#pragma unroll 1
       for (; cur.more() && ok; cur.next(a), ++no) {
         const int t1 = cur.t1();
         if (!W.wait(&sh.o_empty, (no & 1) ^ 1)) break;
+#pragma unroll 1
         for (int j = cur.t0; j < t1; ++j, p.next(), ++i) {
           // the rows cleared by the other CTA's threads want the wider acquire
           if (!(ok = tail(j) ? W.wait_cluster(&sh.v_full[p.s], p.phase) : W.wait(&sh.v_full[p.s], p.phase))) break;
@@ -498,8 +507,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     // Their probabilities are 0, but 0 * NaN is NaN: whatever lies there is cleared.
     RingPos p;
     uint32_t phases = 0;  // of the entries of v_landed, which only some tiles use
+#pragma unroll 1
     for (; cur.more(); cur.next(a)) {
       const int t1 = cur.t1();
+#pragma unroll 1
       for (int j = cur.t0; j < t1 - 1; ++j) p.next();  // only an item's last tile can be its sequence's last
       if (tail(t1 - 1)) {
         if (!W.wait_warp(&sh.v_landed[p.s], (phases >> p.s) & 1)) break;
@@ -586,6 +597,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
       }
       return true;
     };
+#pragma unroll 1
     while (true) {
       const bool more = at.more();
       if (!more && !pending) break;
@@ -608,6 +620,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
       // rescale O, which the tensor cores start on only when it has been read.
       RingPos now = first;
       if (turn != g) now.next();
+#pragma unroll 1
       for (int j = t0 + (turn ^ g);; j += 2) {
         if (pending && (j > t0 || !more) && !(ok = write_rows())) break;
         if (j >= t1) break;

@@ -37,6 +37,7 @@ struct Waiter {
     const uint32_t a = smem_addr(bar);
     if (kCluster ? mbar_try_wait_cluster(a, parity) : mbar_try_wait(a, parity)) return true;
     const uint64_t t0 = global_timer_ns();
+#pragma unroll 1
     while (true) {
       if (kCluster ? mbar_try_wait_cluster(a, parity) : mbar_try_wait(a, parity)) return true;
       if (!drain && aborted()) return false;
@@ -56,11 +57,22 @@ struct Waiter {
   MLA_DEV bool wait_warp(uint64_t* bar, uint32_t parity) { return __all_sync(~0u, wait(bar, parity)); }
 };
 
-// a / b for a >= 0, b > 0; 32-bit where both fit (a 64-bit division takes
-// hundreds of cycles).
+// a / b for a >= 0, b > 0: one 32-bit division where both fit, else bit by bit
+// (a call that long runs for a minute). The compiler's 64-bit division, inlined
+// wherever one is needed, made up a seventh of the attention kernel's code.
 MLA_DEV long long quotient(long long a, long long b) {
   if (((unsigned long long)a | (unsigned long long)b) >> 32 == 0) return (uint32_t)a / (uint32_t)b;
-  return a / b;
+  unsigned long long q = 0, r = 0;
+#pragma unroll 1
+  for (int i = 62; i >= 0; --i) {
+    r = (r << 1) | (((unsigned long long)a >> i) & 1u);
+    q <<= 1;
+    if (r >= (unsigned long long)b) {
+      r -= (unsigned long long)b;
+      q |= 1u;
+    }
+  }
+  return (long long)q;
 }
 
 // Range [*first, *first + return) of sequence b in ragged rows [0, rows):

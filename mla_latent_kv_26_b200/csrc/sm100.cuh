@@ -35,6 +35,16 @@ MLA_DEV uint32_t cluster_id_x() {
   return r;
 }
 
+// True in one lane of the (converged) warp. A thread picked by elect.sync issues
+// tcgen05 and TMA instructions with operands in uniform registers; for one picked
+// by its lane number the compiler moves every operand there first, some 60
+// instructions for an MMA.
+MLA_DEV bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
+}
+
 // Address of the same shared-memory variable in CTA `rank` of the cluster.
 MLA_DEV uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
   uint32_t r;
