@@ -42,7 +42,8 @@
 //                   The tensor core's queue is short, an issuer is held up while
 //                   its products run: with one issuer its own waits and address
 //                   arithmetic then left the tensor cores idle
-//   warp 9          producer by TMA: Q, V of tile i, K of tile i + 3
+//   warp 9          producer by TMA: Q, V of tile i, K of tile i + 3; walks the run
+//                   and hands every item on to the other warps
 //   warp 10         clears the value rows behind a sequence's end
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -72,6 +73,7 @@ constexpr int kStageBytes = kKBytes + kVBytes;
 constexpr int kAttnSmem = 1024 + 2 * kQBytes + kStages * kStageBytes;
 constexpr uint32_t kTmemO = 0, kTmemP = 128, kTmemS = 256, kTmemAll = 512;
 constexpr float kGrowth = 8.0f;            // log2: O is rescaled when a row's maximum grew by more (p stays below 2^8)
+constexpr int kItems = 8;                  // items handed on and not yet finished by every warp
 constexpr int kItemUnits = 3;              // cost of an item beside its tiles, in tiles
 // Registers a thread after the split: the softmax warpgroups hold a row of
 // scores each. 256 * 200 + 128 * 104 = 64512 = the 384 * 168 launched.
@@ -136,6 +138,16 @@ struct Seq {
     const long long k = min((long long)full, max(0ll, -c / 2));
     return k + (full - k) * c + ((long long)full * (full + 1) - k * (k + 1)) + (m == full ? 0 : last);
   }
+};
+
+// A run's part of an item, as the producer hands it to the other warps.
+struct Item {
+  int t0, t1;         // key tiles; t1 = 0: the run's end
+  int q, rows;        // first query row of the block, its rows
+  int h;
+  int L, k0;          // the sequence's keys, the first one's row
+  int sees;           // keys that the query before the block's first sees, when causal
+  int part;           // all of the item's keys: -1; else the slot of its partials (0, 1)
 };
 
 // Position of a run in the list of items. An item takes kItemUnits + tiles units
@@ -274,8 +286,8 @@ struct AttnShared {
   uint64_t v_landed[kStages];                  // V of a sequence's last tile, before its rows are cleared
   uint64_t m_ready[4], fin[4];                 // per 32 rows: reference maximum of a tile, sums of an item
   uint64_t done;
-  Cursor start;
-  Cursor cursor[8];                            // of the softmax warps, which need their registers for scores
+  uint64_t item_full[kItems], item_free[kItems];  // entry of item[], read by all other warps
+  Item item[kItems];
   PendingRows pending[8];
   float m[2][kTile];                           // reference maximum after tile n, entry n % 2
   float fin_m[2][2][kTile], fin_l[2][2][kTile];  // [item % 2][warpgroup]
@@ -345,6 +357,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
       mbar_init(smem_addr(&sh.m_ready[x]), 1);
       mbar_init(smem_addr(&sh.fin[x]), 2);     // the two softmax warps of the rows
     }
+    for (int x = 0; x < kItems; ++x) {
+      mbar_init(smem_addr(&sh.item_full[x]), 1);
+      mbar_init(smem_addr(&sh.item_free[x]), rank == 0 ? 11 : 9);  // softmax, clearing, (even CTA) issuers
+    }
     mbar_init(smem_addr(&sh.done), 2);         // the two issuers
     sh.abort_flag = 0u;
     fence_mbar_init();
@@ -353,82 +369,96 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     tmem_alloc_pair(smem_addr(&sh.tmem), kTmemAll);
     tmem_relinquish_pair();
   }
-  if (warp == 9) {
-    Cursor c;
-    grid_dependency_wait();
-    run_start(a, worker, &c);
-    if (lane == 0) {
-      sh.start = c;
-      if (rank == 0) a.info[worker].pieces = 0;
-      prefetch_tmap(&maps.q);
-      prefetch_tmap(&maps.k);
-      prefetch_tmap(&maps.v);
-      prefetch_tmap(&maps.pe);
-    }
+  if (warp == 9 && elect_one()) {
+    prefetch_tmap(&maps.q);
+    prefetch_tmap(&maps.k);
+    prefetch_tmap(&maps.v);
+    prefetch_tmap(&maps.pe);
   }
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
   grid_dependency_wait();  // every thread, for its own accesses
   const uint32_t tmem = sh.tmem;
-  Cursor cur = sh.start;
   // an entry of the even CTA's barriers, for both CTAs
   const auto leader = [&](uint64_t* bar) { return map_to_rank(smem_addr(bar), 0); };
-  const auto tail = [&](int j) { return cur.s.L < (j + 1) * kTile; };  // tile j reaches behind the sequence's end
+  // tile j reaches behind the sequence's end
+  const auto tail = [](const Item& it, int j) { return it.L < (j + 1) * kTile; };
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   }
   if (warp == 9) {
     // ------------------------------------------------------------ producer
+    Cursor cur;
+    run_start(a, worker, &cur);
     if (elect_one()) {
-      Cursor ahead = cur;  // position of Q and K, three tiles before V
+      if (rank == 0) a.info[worker].pieces = 0;
       RingPos pk, pv;
-      int nq = 0, jk = ahead.t0;
-      bool ok = true;
-      const auto load_k = [&]() {
-        if (!ahead.more()) return true;
-        if (jk == ahead.t0) {
-          const int b = nq & 1;
-          if (!W.wait(&sh.q_empty[b], ((nq >> 1) & 1) ^ 1)) return false;
-          mbar_arrive_expect_tx_cluster(leader(&sh.q_full[b]), kQBytes);
-          tma_load_3d_pair(qbuf + b * kQBytes, &maps.q, 0, ahead.s.q0 + ahead.qb * kBlockQ + rank * kTile, 3 * ahead.h,
-                           leader(&sh.q_full[b]));
-          ++nq;
-        }
-        if (!W.wait(&sh.k_empty[pk.s], pk.phase ^ 1)) return false;  // K of three tiles ago is done with
-        const uint32_t kf = leader(&sh.k_full[pk.s]), ks = stages + pk.s * kStageBytes;
-        const int row = ahead.s.k0 + jk * kTile + 64 * rank;
-        mbar_arrive_expect_tx_cluster(kf, kKBytes);
-        tma_load_3d_pair(ks, &maps.k, 0, row, 4 * ahead.h, kf);
-        tma_load_3d_pair(ks + 2 * kHalfBox, &maps.pe, 0, row, 0, kf);
-        pk.next();
-        if (++jk == ahead.t1()) {
-          ahead.next(a);
-          jk = ahead.t0;
-        }
-        return true;
-      };
+      int nk = 0, nv = 0;           // items handed on, items of V begun
+      int jk = 0, k_end = 0, jv = 0, v_end = 0;  // tiles of the items at hand
+      int left = 0;                 // tiles whose K was loaded and V not yet
+      bool ok = true, more = true;
+      // turn x: V of tile x - 3, K of tile x
 #pragma unroll 1
-      for (int x = 0; x < kStages && ok; ++x) ok = load_k();
-#pragma unroll 1
-      for (; cur.more() && ok; cur.next(a)) {
-        const int t1 = cur.t1();
-#pragma unroll 1
-        for (int j = cur.t0; j < t1; ++j, pv.next()) {
+      for (int x = 0; ok; ++x) {
+        if (x >= kStages) {
+          if (left == 0) break;
+          if (jv == v_end) {
+            const Item& next = sh.item[nv++ % kItems];
+            jv = next.t0;
+            v_end = next.t1;
+          }
+          const Item& it = sh.item[(nv - 1) % kItems];
           if (!(ok = W.wait(&sh.pv_done[pv.s], pv.phase ^ 1))) break;  // V of three tiles ago is done with
           const uint32_t vs = stages + pv.s * kStageBytes + kKBytes;
-          const int row = cur.s.k0 + j * kTile;
-          if (tail(j)) {
+          const int row = it.k0 + jv * kTile;
+          if (tail(it, jv)) {
             const uint32_t vl = smem_addr(&sh.v_landed[pv.s]);
             mbar_arrive_expect_tx(vl, kVBytes);
-            tma_load_3d(vs, &maps.v, 0, row, 4 * cur.h + 2 + rank, vl);
+            tma_load_3d(vs, &maps.v, 0, row, 4 * it.h + 2 + rank, vl);
           } else {
             const uint32_t vf = leader(&sh.v_full[pv.s]);
             mbar_arrive_expect_tx_cluster(vf, kVBytes);
-            tma_load_3d_pair(vs, &maps.v, 0, row, 4 * cur.h + 2 + rank, vf);
+            tma_load_3d_pair(vs, &maps.v, 0, row, 4 * it.h + 2 + rank, vf);
           }
-          if (!(ok = load_k())) break;
+          pv.next();
+          ++jv;
+          --left;
+        }
+        if (more && jk == k_end) {  // the next item, or the run's end, for all warps
+          const int e = nk % kItems, b = nk & 1;
+          if (!(ok = W.wait(&sh.item_free[e], ((nk / kItems) & 1) ^ 1))) break;
+          Item& it = sh.item[e];
+          const int t1 = cur.t1(), r0 = cur.qb * kBlockQ;
+          jk = cur.t0;
+          more = cur.more();
+          it = Item{jk, more ? t1 : 0, cur.s.q0 + r0, min(cur.s.n - r0, kBlockQ), cur.h, cur.s.L, cur.s.k0,
+                    cur.s.L - cur.s.n + r0, jk > 0 ? 0 : t1 < cur.tiles ? 1 : -1};
+          mbar_arrive(smem_addr(&sh.item_full[e]));
+          if (more) {
+            k_end = t1;
+            if (rank == 0 && it.part == 1)  // the item goes on in the following runs
+              a.info[worker] = SplitInfo{
+                  (int)(quotient(cur.item + kItemUnits + cur.tiles - 1, cur.quota) - worker) + 1, it.q, it.rows, it.h};
+            if (!(ok = W.wait(&sh.q_empty[b], ((nk >> 1) & 1) ^ 1))) break;
+            mbar_arrive_expect_tx_cluster(leader(&sh.q_full[b]), kQBytes);
+            tma_load_3d_pair(qbuf + b * kQBytes, &maps.q, 0, it.q + rank * kTile, 3 * it.h, leader(&sh.q_full[b]));
+            ++nk;
+            cur.next(a);
+          }
+        }
+        if (more) {
+          const Item& it = sh.item[(nk - 1) % kItems];
+          if (!(ok = W.wait(&sh.k_empty[pk.s], pk.phase ^ 1))) break;  // K of three tiles ago is done with
+          const uint32_t kf = leader(&sh.k_full[pk.s]), ks = stages + pk.s * kStageBytes;
+          const int row = it.k0 + jk * kTile + 64 * rank;
+          mbar_arrive_expect_tx_cluster(kf, kKBytes);
+          tma_load_3d_pair(ks, &maps.k, 0, row, 4 * it.h, kf);
+          tma_load_3d_pair(ks + 2 * kHalfBox, &maps.pe, 0, row, 0, kf);
+          pk.next();
+          ++jk;
+          ++left;
         }
       }
       // Every load was waited for by its reader, unless a wait ran out: then
@@ -444,15 +474,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     if (rank == 0 && elect_one()) {
       constexpr uint32_t idesc = idesc_bf16_f32(256, 128, 0, 0);
       RingPos p;
-      int nq = 0, i = 0;  // query blocks, tiles
+      int nq = 0, i = 0;  // items, tiles
       bool ok = true;
 #pragma unroll 1
-      for (; cur.more() && ok; cur.next(a), ++nq) {
-        const int t1 = cur.t1(), b = nq & 1;
+      for (; ok; ++nq) {
+        if (!W.wait(&sh.item_full[nq % kItems], (nq / kItems) & 1)) break;
+        const int t0 = sh.item[nq % kItems].t0, t1 = sh.item[nq % kItems].t1, b = nq & 1;
+        if (t1 == 0) break;
+        mbar_arrive(smem_addr(&sh.item_free[nq % kItems]));
         if (!W.wait(&sh.q_full[b], (nq >> 1) & 1)) break;
         const uint64_t qd = smem_desc_sw128(qbuf + b * kQBytes, 16, 1024);
 #pragma unroll 1
-        for (int j = cur.t0; j < t1; ++j, p.next(), ++i) {
+        for (int j = t0; j < t1; ++j, p.next(), ++i) {
           if (!(ok = W.wait(&sh.k_full[p.s], p.phase))) break;
           if (!(ok = W.wait(&sh.s_free[i & 1], ((i >> 1) & 1) ^ 1))) break;
           tc_fence_after();
@@ -480,20 +513,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
       int no = 0, i = 0;  // items, tiles
       bool ok = true;
 #pragma unroll 1
-      for (; cur.more() && ok; cur.next(a), ++no) {
-        const int t1 = cur.t1();
+      for (; ok; ++no) {
+        if (!W.wait(&sh.item_full[no % kItems], (no / kItems) & 1)) break;
+        const Item& it = sh.item[no % kItems];
+        const int t0 = it.t0, t1 = it.t1, last_tail = tail(it, t1 - 1) ? t1 - 1 : -1;
+        if (t1 == 0) break;
+        mbar_arrive(smem_addr(&sh.item_free[no % kItems]));
         if (!W.wait(&sh.o_empty, (no & 1) ^ 1)) break;
 #pragma unroll 1
-        for (int j = cur.t0; j < t1; ++j, p.next(), ++i) {
+        for (int j = t0; j < t1; ++j, p.next(), ++i) {
           // the rows cleared by the other CTA's threads want the wider acquire
-          if (!(ok = tail(j) ? W.wait_cluster(&sh.v_full[p.s], p.phase) : W.wait(&sh.v_full[p.s], p.phase))) break;
+          if (!(ok = j == last_tail ? W.wait_cluster(&sh.v_full[p.s], p.phase) : W.wait(&sh.v_full[p.s], p.phase))) break;
           if (!(ok = W.wait(&sh.p_full[i & 1], (i >> 1) & 1))) break;
           tc_fence_after();
           const uint64_t vd = smem_desc_sw128(stages + p.s * kStageBytes + kKBytes, kBox, 1024);
           const uint32_t pt = tmem + kTmemP + 64 * (i & 1);
 #pragma unroll
           for (int u = 0; u < 8; ++u)  // 16 keys: 8 columns of P, 16 rows of V
-            mma_tmem_a_pair(tmem + kTmemO, pt + 8 * u, vd + 128 * u, idesc, (u > 0 || j > cur.t0) ? 1u : 0u);
+            mma_tmem_a_pair(tmem + kTmemO, pt + 8 * u, vd + 128 * u, idesc, (u > 0 || j > t0) ? 1u : 0u);
           mma_commit_pair(smem_addr(&sh.pv_done[p.s]));
         }
         if (ok) mma_commit_pair(smem_addr(&sh.o_done));
@@ -508,15 +545,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     RingPos p;
     uint32_t phases = 0;  // of the entries of v_landed, which only some tiles use
 #pragma unroll 1
-    for (; cur.more(); cur.next(a)) {
-      const int t1 = cur.t1();
+    for (int n = 0;; ++n) {
+      if (!W.wait_warp(&sh.item_full[n % kItems], (n / kItems) & 1)) break;
+      const Item it = sh.item[n % kItems];
+      const int t1 = it.t1;
+      if (t1 == 0) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&sh.item_free[n % kItems]));
 #pragma unroll 1
-      for (int j = cur.t0; j < t1 - 1; ++j) p.next();  // only an item's last tile can be its sequence's last
-      if (tail(t1 - 1)) {
+      for (int j = it.t0; j < t1 - 1; ++j) p.next();  // only an item's last tile can be its sequence's last
+      if (tail(it, t1 - 1)) {
         if (!W.wait_warp(&sh.v_landed[p.s], (phases >> p.s) & 1)) break;
         phases ^= 1u << p.s;
         const uint32_t vs = stages + p.s * kStageBytes + kKBytes;
-        for (int x = max(cur.s.L - (t1 - 1) * kTile, 0) * 8 + lane; x < kTile * 8; x += 32)
+        for (int x = max(it.L - (t1 - 1) * kTile, 0) * 8 + lane; x < kTile * 8; x += 32)
           st_shared_v4(vs + 16 * x, make_uint4(0, 0, 0, 0));
         fence_proxy_async_smem();
         __syncwarp();
@@ -536,12 +578,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     RingPos mine;                                      // entry of this warpgroup's last tile
     int turn = 0;                                      // tiles before the item, mod 2
     int ns = 0;                                        // tiles of this warpgroup
+    int ne = 0;                                        // items
     int nm = 0, nf = 0, ni = 0;                        // tiles with shared maxima; written items with live rows, all items
     bool ok = true;
     bool pending = false;                              // an item's rows are still to be written
-    Cursor& at = sh.cursor[warp];
-    at = cur;                                          // every lane writes, and reads, the same
-    __syncwarp();
     // The rows of an item, or this run's part of them: 64 columns for each
     // warpgroup. The last P V is normally long done when this is called.
     const auto write_rows = [&]() {
@@ -554,13 +594,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
         if (lane == 0) mbar_arrive_cluster(leader(&sh.o_empty));
         return true;
       }
-      uint32_t o[2][32];
-      tmem_ld_32x32b_32(lanes + kTmemO + 64 * g, o[0]);
-      tmem_ld_32x32b_32(lanes + kTmemO + 64 * g + 32, o[1]);
-      tmem_wait_ld();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(leader(&sh.o_empty));
       if (!W.wait_warp(&sh.fin[quad], nf & 1)) return false;
       const float m0 = sh.fin_m[nf & 1][0][row], m1 = sh.fin_m[nf & 1][1][row], mm = fmaxf(m0, m1);
       const float l0 = sh.fin_l[nf & 1][0][row], l1 = sh.fin_l[nf & 1][1][row];
@@ -569,50 +602,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
       if (l1 > 0.f) l += l1 * ex2((m1 - mm) * a.scale_log2);
       const float inv = l > 0.f ? 1.f / l : 0.f;       // a row without keys: its products are all 0 * v
       const float lse = l > 0.f ? mm * a.scale + logf(l) : -INFINITY;
-      if (lane >= pr.rows) return true;
-      if (pr.whole) {
-        const size_t r = (size_t)(pr.q + lane) * a.heads + pr.h;
-        __nv_bfloat16* dst = a.out + r * 128 + 64 * g;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          uint32_t w[8];
+      const bool valid = lane < pr.rows;
+      const size_t r = (size_t)(pr.q + lane) * a.heads + pr.h, prow = (size_t)pr.part + lane;
+      __nv_bfloat16* dst = a.out + r * 128 + 64 * g;
+      float* part = a.part_o + prow * 128 + 64 * g;
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t o[16];
+        tmem_ld_32x32b_16(lanes + kTmemO + 64 * g + 16 * c, o);
+        tmem_wait_ld();
+        if (c == 3) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(leader(&sh.o_empty));
+        }
+        if (!valid) continue;
+        uint32_t w[8];
+        if (pr.whole) {
 #pragma unroll
           for (int x = 0; x < 8; ++x)
-            w[x] = pack_bf16x2(__uint_as_float(o[u >> 1][16 * (u & 1) + 2 * x]) * inv,
-                               __uint_as_float(o[u >> 1][16 * (u & 1) + 2 * x + 1]) * inv);
-          st_global_v8(dst + 16 * u, w);
-        }
-        if (g == 0) a.lse[r] = lse;
-      } else {
-        const size_t prow = (size_t)pr.part + lane;
-        float* dst = a.part_o + prow * 128 + 64 * g;
+            w[x] = pack_bf16x2(__uint_as_float(o[2 * x]) * inv, __uint_as_float(o[2 * x + 1]) * inv);
+          st_global_v8(dst + 16 * c, w);
+        } else {
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          uint32_t w[8];
+          for (int h = 0; h < 2; ++h) {
 #pragma unroll
-          for (int x = 0; x < 8; ++x) w[x] = __float_as_uint(__uint_as_float(o[u >> 2][8 * (u & 3) + x]) * inv);
-          st_global_v8(dst + 8 * u, w);
+            for (int x = 0; x < 8; ++x) w[x] = __float_as_uint(__uint_as_float(o[8 * h + x]) * inv);
+            st_global_v8(part + 16 * c + 8 * h, w);
+          }
         }
-        if (g == 0) a.part_lse[prow] = lse;
+      }
+      if (valid && g == 0) {
+        if (pr.whole) a.lse[r] = lse;
+        else a.part_lse[prow] = lse;
       }
       return true;
     };
 #pragma unroll 1
     while (true) {
-      const bool more = at.more();
+      if (!(ok = W.wait_warp(&sh.item_full[ne % kItems], (ne / kItems) & 1))) break;
+      const Item& it = sh.item[ne % kItems];
+      const int t0 = it.t0, t1 = it.t1;
+      const bool more = t1 > 0;
       if (!more && !pending) break;
-      const int t0 = more ? at.t0 : 0, t1 = more ? at.t1() : 0, r0 = at.qb * kBlockQ + kTile * rank;
-      if (rank == 0 && threadIdx.x == 0 && more && t0 == 0 && t1 < at.tiles) {
-        // the item goes on in the following runs
-        const long long last = quotient(at.item + kItemUnits + at.tiles - 1, at.quota);
-        a.info[worker] = SplitInfo{(int)(last - worker) + 1, at.s.q0 + at.qb * kBlockQ,
-                                   min(at.s.n - at.qb * kBlockQ, kBlockQ), at.h};
-      }
       // keys this row sees
-      const int limit = a.causal ? min(at.s.L, at.s.L - at.s.n + r0 + row + 1) : at.s.L;
+      const int limit = a.causal ? min(it.L, it.sees + kTile * rank + row + 1) : it.L;
       // key tiles that all of the warp's rows see whole (the first row sees least)
       const int whole_tiles = __shfl_sync(~0u, limit, 0) >> 7;
-      const bool live = r0 < at.s.n;                   // without live rows only the hand-shakes remain
+      const bool live = kTile * rank < it.rows;        // without live rows only the hand-shakes remain
       float m = -INFINITY, l = 0.f;                    // this warpgroup's reference maximum (raw scores) and sum
       // This warpgroup's tiles, every second one, and one turn behind the last.
       // The rows of the item before are written when the item's first tile is
@@ -641,10 +678,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
           if (j >= whole_tiles) {
             const int seen = limit - j * kTile;
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+            for (int c = 0; c < 4; ++c) {
+              const int n = min(max(seen - 32 * c, 0), 32);
+              const uint32_t hidden = n < 32 ? ~0u << n : 0u;  // bit x: column 32 c + x is not seen
 #pragma unroll
               for (int x = 0; x < 32; ++x)
-                if (32 * c + x >= seen) s[c][x] = 0xff800000u;  // -inf
+                if ((hidden >> x) & 1u) s[c][x] = 0xff800000u;  // -inf
+            }
           }
           float mx[4];
 #pragma unroll
@@ -673,13 +713,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
             if (!(ok = W.wait_warp(&sh.pv_done[prev.s], prev.phase ^ 1))) break;
             tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              uint32_t o[32];
-              tmem_ld_32x32b_32(lanes + kTmemO + 32 * c, o);
+            for (int c = 0; c < 8; ++c) {
+              uint32_t o[16];
+              tmem_ld_32x32b_16(lanes + kTmemO + 16 * c, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-              tmem_st_32(lanes + kTmemO + 32 * c, o);
+              for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+              tmem_st_16(lanes + kTmemO + 16 * c, o);
             }
           }
           const float shift = m == -INFINITY ? 0.f : -m * a.scale_log2;
@@ -731,18 +771,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
         sh.fin_l[nf & 1][g][row] = l;
       }
       if (lane == 0) {
-        const int q = r0 + quad * 32;
-        const long long slot = 2ll * worker + (t0 == 0 ? 1 : 0);
-        sh.pending[warp] = PendingRows{at.s.q0 + q, at.s.n - q, at.h, live, t0 == 0 && t1 == at.tiles,
-                                       slot * kBlockQ + kTile * rank + quad * 32};
+        const int r0 = kTile * rank + quad * 32;
+        sh.pending[warp] = PendingRows{it.q + r0, it.rows - r0, it.h, live, it.part < 0,
+                                       (2ll * worker + it.part) * kBlockQ + r0};
+        mbar_arrive(smem_addr(&sh.item_free[ne % kItems]));
       }
+      ++ne;
       __syncwarp();
       if (live && lane == 0) mbar_arrive(smem_addr(&sh.fin[quad]));
-      Cursor next = at;
-      next.next(a);
-      __syncwarp();
-      at = next;
-      __syncwarp();
     }
     __syncwarp();
   }
