@@ -3,6 +3,9 @@
 * :mod:`.binding`   — ctypes binding of the C ABI in ``include/mla.h``
   (``mla_decode_plan`` / ``mla_decode`` / ``mla_combine`` / ...).
 * :mod:`.decoder`   — ``MlaDecoder``: buffers plus the three calls on a stream.
+* :mod:`.prefill`   — ``MlaPrefill``: attention of a chunk of new tokens over
+  the paged cache (``include/mla_prefill.h``: cache read-back, key / value
+  expansion, ragged attention).
 * :mod:`.workloads` — seeded synthetic inputs.
 * :mod:`.build`     — builds ``libmla.so`` in-tree with nvcc.
 
@@ -25,4 +28,8 @@ def __getattr__(name):
         from . import decoder
 
         return getattr(decoder, name)
+    if name in ("MlaPrefill", "cache_read", "expand_kv", "prefill_attention", "merge_parts"):
+        from . import prefill
+
+        return getattr(prefill, name)
     raise AttributeError(name)

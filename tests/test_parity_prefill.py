@@ -445,3 +445,92 @@ def test_two_streams_at_once(dev):
     torch.cuda.synchronize(dev)
     for p, x in zip(pres, want):
         assert torch.equal(p.out[:x.shape[0]], x)
+
+
+def test_more_tokens_than_capacity_is_clipped_and_reported(dev, libmla):
+    """Offsets beyond MlaPrefill's buffers touch nothing outside them; the error word says so."""
+    from mla_latent_kv_26_b200.prefill import MlaPrefill
+
+    cache, bt, q, w, cu_q, cu_k = _chunk([(40, 200), (30, 90)], 2, 61, False)
+    g = [t.to(dev) for t in (q, w, cache, bt, cu_q, cu_k)]
+    pre = MlaPrefill(max_queries=70, max_keys=150, num_heads=2, device=dev)
+    pre(*g)
+    assert int(pre.error_word.item()) == libmla.MLA_DEVERR_SEQ_LEN
+    with pytest.raises(ValueError):
+        MlaPrefill(max_queries=69, max_keys=290, num_heads=2, device=dev)(*g)
+    # within its capacity the same object is fine afterwards
+    pre.error_word.zero_()
+    cache, bt, q, w, cu_q, cu_k = _chunk([(40, 100), (30, 50)], 2, 62, False)
+    out = pre(q.to(dev), w.to(dev), cache.to(dev), bt.to(dev), cu_q.to(dev), cu_k.to(dev))
+    assert int(pre.error_word.item()) == 0
+    _check_chunk(out, pre.lse[:70], cache, bt, q, w, cu_q, cu_k)
+
+
+# ---------------------------------------------------------------- far rows
+
+
+def test_rows_beyond_four_gigabytes(dev):
+    """Cache pages, rows, keys / values and queries whose byte offsets pass 2^32."""
+    from mla_latent_kv_26_b200.prefill import cache_read, expand_kv, prefill_attention
+
+    g = torch.Generator().manual_seed(71)
+    pages = 60000                                        # 4.4 GB of cache
+    cache = torch.empty(pages, 64, 576, dtype=torch.bfloat16, device=dev)
+    last = torch.randn(2, 64, 576, generator=g).to(torch.bfloat16)
+    cache[-2:] = last.to(dev)
+    bt = torch.tensor([[pages - 1, pages - 2]], dtype=torch.int32, device=dev)
+    rows = cache_read(cache, bt, torch.tensor([0, 128], dtype=torch.int32, device=dev), num_rows=128)
+    assert torch.equal(rows.cpu(), torch.cat([last[1], last[0]]))
+    del cache
+
+    H, M = 128, 66000                                    # 4.3 GB of keys and values, 3.2 GB of queries
+    x = torch.zeros(M, 576, dtype=torch.bfloat16, device=dev)
+    x[-128:] = rows
+    w = (torch.randn(H, 256, 512, generator=g) * 0.05).to(torch.bfloat16)
+    kv = expand_kv(x, w.to(dev))
+    tail = kv[-128:].double().cpu()
+    ref = oracle.prefill.expand_kv(rows.cpu(), w)
+    mag = oracle.prefill.expand_kv(rows.cpu().abs(), w.abs())
+    assert ((tail - ref).abs() <= ref.abs() * 2.0 ** -8 + mag * 2.0 ** -14).all()
+    assert torch.all(kv[:M - 128] == 0)
+
+    nq = 90000                                           # 4.4 GB of queries
+    q = torch.zeros(nq, H, 192, dtype=torch.bfloat16, device=dev)
+    some = torch.randn(70, H, 192, generator=g).to(torch.bfloat16)
+    q[-70:] = some.to(dev)
+    cu_q = torch.tensor([nq - 70, nq], dtype=torch.int32, device=dev)
+    cu_k = torch.tensor([M - 128, M], dtype=torch.int32, device=dev)
+    out, lse = prefill_attention(q, kv, x[:, 512:], cu_q, cu_k)
+    _check_attention(out[-70:, :4], lse[-70:, :4], some[:, :4], kv[-128:, :4].cpu(), x[-128:, 512:].cpu(),
+                     torch.tensor([0, 70]), torch.tensor([0, 128]), True, oracle.DEFAULT_SOFTMAX_SCALE)
+
+
+@pytest.mark.parametrize("heads,seqs,causal", [(128, [(300, 2300), (513, 1100)], True), (40, [(1030, 1030)], True),
+                                               (24, [(257, 3000)], False)])
+def test_attention_sampled_heads_of_larger_calls(dev, heads, seqs, causal):
+    """Calls large enough for runs of many items and groups of heads; a few heads against the oracle."""
+    from mla_latent_kv_26_b200.prefill import prefill_attention
+
+    q, kv, pe, cu_q, cu_k = _attention_inputs(heads, seqs, 81)
+    err = torch.zeros(1, dtype=torch.int32, device=dev)
+    out, lse = prefill_attention(q.to(dev), kv.to(dev), pe.to(dev), cu_q.to(dev), cu_k.to(dev), causal=causal,
+                                 error_word=err)
+    assert int(err.item()) == 0
+    pick = sorted({0, heads // 2 + 1, heads - 1})
+    _check_attention(out[:, pick], lse[:, pick], q[:, pick], kv[:, pick], pe, cu_q, cu_k, causal,
+                     oracle.DEFAULT_SOFTMAX_SCALE)
+
+
+def test_calls_on_a_stream_of_their_own(dev):
+    """Buffers allocated by the call itself, on the stream it was given."""
+    from mla_latent_kv_26_b200.prefill import cache_read, expand_kv, prefill_attention
+
+    cache, bt, q, w, cu_q, cu_k = _chunk([(100, 300)], 4, 91, True)
+    s = torch.cuda.Stream(dev)
+    with torch.cuda.stream(s):
+        c, b, qg, wg, cq, ck = (t.to(dev) for t in (cache, bt, q, w, cu_q, cu_k))
+        rows = cache_read(c, b, ck, num_rows=300)
+        kv = expand_kv(rows, wg)
+        out, lse = prefill_attention(qg, kv, rows[:, 512:], cq, ck)
+    s.synchronize()
+    _check_chunk(out, lse, cache, bt, q, w, cu_q, cu_k)
