@@ -195,15 +195,21 @@ struct Cursor {
 // Run `w`: called by a whole warp. Two passes over the sequences, 32 at a time.
 MLA_DEV void run_start(const AttnArgs& a, int w, Cursor* cur) {
   const int lane = threadIdx.x & 31;
-  long long total = 0;
+  long long total = 0, first_units = 0;
+  Seq first{0, 0, 0, 0};  // this lane's sequence of the first 32
   bool bad = false;
 #pragma unroll 1
   for (int b = lane; b < a.batch; b += 32) {
     Seq s;
     s.load(a, b);
-    total += s.units_before(s.blocks(), a.causal) * a.heads;
+    const long long units = s.units_before(s.blocks(), a.causal) * a.heads;
     const int oq = __ldg(a.cu_q + b), ok = __ldg(a.cu_k + b);
     bad |= oq != s.q0 || ok != s.k0 || __ldg(a.cu_q + b + 1) != s.q0 + s.n || __ldg(a.cu_k + b + 1) != s.k0 + s.L;
+    if (b == lane) {
+      first = s;
+      first_units = units;
+    }
+    total += units;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(~0u, total, o);
@@ -221,10 +227,13 @@ MLA_DEV void run_start(const AttnArgs& a, int w, Cursor* cur) {
   long long before = 0;
 #pragma unroll 1
   for (int b0 = 0; b0 < a.batch; b0 += 32) {
-    Seq s{0, 0, 0, 0};
-    const int b = b0 + lane;
-    if (b < a.batch) s.load(a, b);
-    const long long own = s.units_before(s.blocks(), a.causal) * a.heads;
+    Seq s = first;
+    long long own = first_units;
+    if (b0 > 0) {
+      s = Seq{0, 0, 0, 0};
+      if (b0 + lane < a.batch) s.load(a, b0 + lane);
+      own = s.units_before(s.blocks(), a.causal) * a.heads;
+    }
     long long incl = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -594,6 +603,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
         if (lane == 0) mbar_arrive_cluster(leader(&sh.o_empty));
         return true;
       }
+      const bool valid = lane < pr.rows;
+      const size_t r = (size_t)(pr.q + lane) * a.heads + pr.h, prow = (size_t)pr.part + lane;
+      __nv_bfloat16* dst = a.out + r * 128 + 64 * g;
+      float* part = a.part_o + prow * 128 + 64 * g;
+      uint32_t o[64];
+      tmem_ld_32x32b_32(lanes + kTmemO + 64 * g, *reinterpret_cast<uint32_t(*)[32]>(&o[0]));
+      tmem_ld_32x32b_32(lanes + kTmemO + 64 * g + 32, *reinterpret_cast<uint32_t(*)[32]>(&o[32]));
+      tmem_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(leader(&sh.o_empty));
       if (!W.wait_warp(&sh.fin[quad], nf & 1)) return false;
       const float m0 = sh.fin_m[nf & 1][0][row], m1 = sh.fin_m[nf & 1][1][row], mm = fmaxf(m0, m1);
       const float l0 = sh.fin_l[nf & 1][0][row], l1 = sh.fin_l[nf & 1][1][row];
@@ -602,34 +622,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
       if (l1 > 0.f) l += l1 * ex2((m1 - mm) * a.scale_log2);
       const float inv = l > 0.f ? 1.f / l : 0.f;       // a row without keys: its products are all 0 * v
       const float lse = l > 0.f ? mm * a.scale + logf(l) : -INFINITY;
-      const bool valid = lane < pr.rows;
-      const size_t r = (size_t)(pr.q + lane) * a.heads + pr.h, prow = (size_t)pr.part + lane;
-      __nv_bfloat16* dst = a.out + r * 128 + 64 * g;
-      float* part = a.part_o + prow * 128 + 64 * g;
-#pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        uint32_t o[16];
-        tmem_ld_32x32b_16(lanes + kTmemO + 64 * g + 16 * c, o);
-        tmem_wait_ld();
-        if (c == 3) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(leader(&sh.o_empty));
-        }
-        if (!valid) continue;
+      if (valid) {
+#pragma unroll
+        for (int x = 0; x < 64; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * inv);
         uint32_t w[8];
         if (pr.whole) {
 #pragma unroll
-          for (int x = 0; x < 8; ++x)
-            w[x] = pack_bf16x2(__uint_as_float(o[2 * x]) * inv, __uint_as_float(o[2 * x + 1]) * inv);
-          st_global_v8(dst + 16 * c, w);
+          for (int c = 0; c < 4; ++c) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              w[x] = pack_bf16x2(__uint_as_float(o[16 * c + 2 * x]), __uint_as_float(o[16 * c + 2 * x + 1]));
+            st_global_v8(dst + 16 * c, w);
+          }
         } else {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-#pragma unroll
-            for (int x = 0; x < 8; ++x) w[x] = __float_as_uint(__uint_as_float(o[8 * h + x]) * inv);
-            st_global_v8(part + 16 * c + 8 * h, w);
-          }
+          for (int c = 0; c < 8; ++c) st_global_v8(part + 8 * c, *reinterpret_cast<uint32_t(*)[8]>(&o[8 * c]));
         }
       }
       if (valid && g == 0) {
