@@ -19,7 +19,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libmla.so")
 SOURCES = ["mla_api.cu", "mla_decode.cu", "mla_plan_combine.cu", "mla_insert.cu", "mla_absorb.cu",
            "mla_indexer.cu", "mla_cache_read.cu", "mla_expand_kv.cu", "mla_prefill_attention.cu"]
-HEADERS = ["common.cuh", "sm100.cuh", "prefill.cuh"]
+HEADERS = ["common.cuh", "sm100.cuh", "prefill.cuh", "prefill_ptx.cuh"]
 PUBLIC_HEADERS = ["mla.h", "mla_prefill.h"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 

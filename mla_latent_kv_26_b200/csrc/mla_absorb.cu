@@ -77,6 +77,18 @@ MLA_DEV bool wait_bounded(uint32_t bar, uint32_t parity) {
   return true;
 }
 
+// 32x32b shape, 32 columns: thread i of the warp reads TMEM lane (base lane + i).
+MLA_DEV void tmem_ld_32x32b_32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+
 // 32 fp32 accumulator columns of this thread's row -> 32 bf16 at dst (64 B).
 MLA_DEV void store_row_bf16(__nv_bfloat16* dst, const uint32_t (&r)[32]) {
   uint4* d = reinterpret_cast<uint4*>(dst);
@@ -87,6 +99,16 @@ MLA_DEV void store_row_bf16(__nv_bfloat16* dst, const uint32_t (&r)[32]) {
                       pack_bf16x2(__uint_as_float(r[8 * u + 4]), __uint_as_float(r[8 * u + 5])),
                       pack_bf16x2(__uint_as_float(r[8 * u + 6]), __uint_as_float(r[8 * u + 7])));
 }
+
+// TMA store of a 2-D box from shared memory (completion tracked by the
+// issuing thread's bulk async-group).
+MLA_DEV void tma_store_2d(const CUtensorMap* map, uint32_t src, int32_t c0, int32_t c1) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(c0),
+               "r"(c1), "r"(src)
+               : "memory");
+}
+MLA_DEV void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+MLA_DEV void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 
 // The epilogue's staging: this thread's TMEM lane (token row `row`) holds
 // 32 * nchunks fp32 columns; they are rounded to bf16 and written as row

@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(256) mla_combine_kernel(CombineArgs a) {
 // Merge of `parts` results of the same rows computed over disjoint token
 // sets (one per context-parallel shard, or per part of a long context): lanes
 // of a warp hold 8 columns each, so that a 512-wide row takes a warp twice
-// and a 128-wide row half a warp once.
+// and a 128-wide row half a warp once (rows of part_out and out are kWidth wide).
 // lse = M + ln sum_i exp(lse_i - M), out = sum_i exp(lse_i - lse) * out_i;
 // parts with lse_i = -inf weigh nothing; all empty: out = 0, lse = -inf.
 template <int kWidth>

@@ -6,12 +6,10 @@
 #include <stdint.h>
 
 #include "common.cuh"
-#include "sm100.cuh"
+#include "prefill_ptx.cuh"
 
 namespace mla {
 namespace prefill {
-
-using namespace ptx;
 
 constexpr uint32_t kErrPosition = 0x10u;       // MLA_DEVERR_POSITION
 constexpr uint64_t kWaitNs = 2000000000ull;    // a pipeline wait gives up after 2 s: only a broken device gets there
