@@ -9,7 +9,9 @@ latent cache, in three library calls (``include/mla_prefill.h``).
 The wrappers check dtypes, shapes and devices and pass raw pointers; all
 arithmetic happens in libmla's kernels. Offsets and lengths stay on the
 device, nothing synchronises, and a captured CUDA graph replays with other
-lengths within the same capacities.
+lengths within the same capacities. ``stream`` (a torch stream or a raw handle;
+the current one when not given) is where a call's kernels run and where what it
+allocates belongs; inputs made on another stream are the caller's to order.
 
 Sequence b's new tokens are rows ``[cu_q[b], cu_q[b + 1])`` of ``q`` and its
 keys rows ``[cu_k[b], cu_k[b + 1])`` of ``kv``: all its tokens, the new ones
@@ -73,6 +75,16 @@ def _stream(stream, dev):
     return torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream
 
 
+def _allocate(stream, dev, *shape, dtype):
+    """A tensor that belongs to the stream the kernels are launched on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
 def _check_cache(kv_cache, block_table, row_offsets, starts, dev):
     """(fp8, batch) of a paged cache and its tables."""
     if not isinstance(kv_cache, torch.Tensor) or not isinstance(block_table, torch.Tensor):
@@ -123,7 +135,7 @@ def cache_read(kv_cache: torch.Tensor, block_table: torch.Tensor, row_offsets: t
     if out is None:
         if num_rows is None:
             raise ValueError("cache_read needs out or num_rows")
-        out = torch.empty(num_rows, 576, dtype=_BF16, device=dev)
+        out = _allocate(stream, dev, num_rows, 576, dtype=_BF16)
     elif out.dim() != 2:
         raise ValueError("out: need a [rows, 576] tensor")
     _check("out", out, _BF16, (out.shape[0], 576), dev)
@@ -146,7 +158,7 @@ def expand_kv(rows: torch.Tensor, wkv_b: torch.Tensor, *, out: Optional[torch.Te
     _optional_i32("row_count", row_count, dev)
     _optional_i32("error_word", error_word, dev)
     if out is None:
-        out = torch.empty(M, H, 256, dtype=_BF16, device=dev)
+        out = _allocate(stream, dev, M, H, 256, dtype=_BF16)
     _check("out", out, _BF16, (M, H, 256), dev)
     with _on(dev):
         B.check(B.mlap_expand_kv(B.mlap_expand_desc_t(M, H, stride, 128, 512, 128), rows, wkv_b, row_count, out,
@@ -197,9 +209,9 @@ def prefill_attention(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, cu_
     _check("cu_k", cu_k, _I32, cu_q.shape, dev)
     _optional_i32("error_word", error_word, dev)
     if out is None:
-        out = torch.empty(Nq, H, 128, dtype=_BF16, device=dev)
+        out = _allocate(stream, dev, Nq, H, 128, dtype=_BF16)
     if lse is None:
-        lse = torch.empty(Nq, H, dtype=_F32, device=dev)
+        lse = _allocate(stream, dev, Nq, H, dtype=_F32)
     _check("out", out, _BF16, (Nq, H, 128), dev)
     _check("lse", lse, _F32, (Nq, H), dev)
     desc = B.mlap_attention_desc_t(cu_q.shape[0] - 1, H, Nq, Nk, stride, int(bool(causal)), softmax_scale, num_sms,
@@ -207,8 +219,7 @@ def prefill_attention(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, cu_
     with _on(dev):
         if workspace is None:
             n = max(B.mlap_attention_workspace_bytes(desc), 32)
-            with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
-                workspace = torch.empty(n, dtype=_U8, device=dev)
+            workspace = _allocate(stream, dev, n, dtype=_U8)
         _check("workspace", workspace, _U8, None, dev)
         B.check(B.mlap_attention(desc, q, kv, k_pe, cu_q, cu_k, out, lse, workspace, workspace.numel(), error_word,
                                  _stream(stream, dev)), "mlap_attention")
@@ -224,9 +235,9 @@ def merge_parts(part_out: torch.Tensor, part_lse: torch.Tensor, *, stream=None) 
     _check("part_lse", part_lse, torch.float32, tuple(part_out.shape[:-1]), dev)
     if part_out.dim() < 2 or part_out.shape[-1] != 128:
         raise ValueError("part_out: need [parts, ..., 128]")
-    out = torch.empty(part_out.shape[1:], dtype=torch.bfloat16, device=dev)
-    lse = torch.empty(part_lse.shape[1:], dtype=torch.float32, device=dev)
-    with torch.cuda.device(dev):
+    out = _allocate(stream, dev, *part_out.shape[1:], dtype=_BF16)
+    lse = _allocate(stream, dev, *part_lse.shape[1:], dtype=_F32)
+    with _on(dev):
         B.check(B.mla_merge(B.make_merge_desc(parts=part_out.shape[0], rows=lse.numel(), d_latent=128), part_out,
                             part_lse, out, lse, _stream(stream, dev)), "mla_merge")
     return out, lse
@@ -234,7 +245,8 @@ def merge_parts(part_out: torch.Tensor, part_lse: torch.Tensor, *, stream=None) 
 
 class MlaPrefill:
     """The prefill of ragged chunks over the paged cache: read back, expand,
-    attend. Owns the buffers for up to ``max_queries`` new tokens and
+    attend. Keys and values are rounded to bf16 in between (2^-8 of each value at
+    most), as a bf16 kv up-projection of the model makes them. Owns the buffers for up to ``max_queries`` new tokens and
     ``max_keys`` cached tokens (all sequences of a call together; 512 * H + 1152
     bytes per key); a call with more is clipped and sets a bit of ``error_word``."""
 

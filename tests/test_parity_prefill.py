@@ -534,3 +534,21 @@ def test_calls_on_a_stream_of_their_own(dev):
         out, lse = prefill_attention(qg, kv, rows[:, 512:], cq, ck)
     s.synchronize()
     _check_chunk(out, lse, cache, bt, q, w, cu_q, cu_k)
+
+
+def test_stream_argument_as_object_and_as_handle(dev):
+    from mla_latent_kv_26_b200.prefill import cache_read, expand_kv, merge_parts, prefill_attention
+
+    cache, bt, q, w, cu_q, cu_k = _chunk([(60, 150)], 2, 92, False)
+    g = [t.to(dev) for t in (cache, bt, q, w, cu_q, cu_k)]
+    s = torch.cuda.Stream(dev)
+    torch.cuda.synchronize(dev)
+    for stream in (s, s.cuda_stream):
+        rows = cache_read(g[0], g[1], g[5], num_rows=150, stream=stream)
+        kv = expand_kv(rows, g[3], stream=stream)
+        out, lse = prefill_attention(g[2], kv, rows[:, 512:], g[4], g[5], stream=stream)
+        s.synchronize()
+        _check_chunk(out, lse, cache, bt, q, w, cu_q, cu_k)
+        merged, mlse = merge_parts(out[None].contiguous(), lse[None].contiguous(), stream=stream)
+        s.synchronize()
+        assert torch.equal(merged, out) and torch.allclose(mlse, lse, atol=1e-6)
