@@ -12,13 +12,20 @@
 // tiles (Q, filling the pipeline, its rows; without them the runs of six prompts
 // of 645 to 1491 tokens, 16 heads, took from 52 to 93 us, and the call 90 us
 // instead of 78). All units are laid end to end and cut into one equal run per
-// CTA pair, so that every SM gets the same work whatever the lengths. The order is (sequence, group of heads, block, head of the group, tile), with
-// groups of about as many heads as a run has items: pairs then work on the
-// different blocks of one sequence with the same heads, and so the same keys,
-// at about the same time, and share them in L2. (2048 queries over 16384
-// keys of 128 heads: 5.9 GB read from HBM for 1.2 GB of inputs; with all heads in
-// one group 7.7 GB, and 2.50 ms instead of 2.27.) An item cut by a run boundary leaves float32 partials with their own
-// lse, merged by the second kernel.
+// CTA pair, so that every SM gets the same work whatever the lengths. The order
+// is (sequence, group of heads, block, head of the group, tile), with groups of
+// about as many heads as a run has items: pairs then work on the different
+// blocks of one sequence with the same heads, and so the same keys, at about the
+// same time, and share them in L2 (128 heads, 2048 queries over 16384 keys: 2.27
+// ms, 2.50 with all heads in one group). An item cut by a run boundary leaves
+// float32 partials with their own lse, merged by the second kernel.
+// Where keys and values are more than L2 keeps, whole items are dealt in rounds
+// before the runs (rounds_of), which keeps the pairs in step: the same call reads
+// 1.8 GB from HBM instead of 5.9, for 1.2 GB of inputs, and takes 2.14 ms instead
+// of 2.35; 16 heads, 16384 new tokens: 0.97 ms instead of 1.12. With two or three
+// blocks the keys are read too few times for that to pay: 600 queries over 7000
+// keys, 128 heads, 371 us in rounds, 357 in runs; with four (1024 over 8192)
+// within 1 % not causal, 484 us instead of 501 causal.
 //
 // A CTA pair (cta_group::2) works on a block: S = Q K^T and O += P V with M 256,
 // 128 rows in each CTA. Each CTA loads half of every key tile (64 keys of K,
@@ -49,7 +56,7 @@
 // Bound by the tensor cores and the softmax behind them: 1280 cycles of products
 // a tile, about 1650 taken (a warpgroup needs 2900 for its tile, 1024 of them
 // exponentials, every second tile is its). 2048 queries over 16384 keys, 128
-// heads, causal: 2.39 ms, 1.08 PFLOP/s at 1.2 to 1.3 GHz under the power cap;
+// heads, causal: 2.17 ms, 1.19 PFLOP/s at 1.2 to 1.3 GHz under the power cap;
 // 2048 over 8192 keys, 32 heads: 242 us, 1.24 PFLOP/s, tensor pipe 71 % active.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -80,6 +87,9 @@ constexpr int kAttnSmem = 1024 + 2 * kQBytes + kStages * kStageBytes;
 constexpr uint32_t kTmemO = 0, kTmemP = 128, kTmemS = 256, kTmemAll = 512;
 constexpr float kGrowth = 8.0f;            // log2: O is rescaled when a row's maximum grew by more (p stays below 2^8)
 constexpr int kItems = 8;                  // items handed on and not yet finished by every warp
+constexpr long long kShareBytes = 64ll << 20;  // keys and values that would not stay in L2 (126 MB)
+constexpr int kShareBlocks = 4;            // and that are read by so many blocks
+constexpr int kKeyBytes = 512;             // of a head's key and value
 constexpr int kItemUnits = 3;              // cost of an item beside its tiles, in tiles
 // Registers a thread after the split: the softmax warpgroups hold a row of
 // scores each. 256 * 200 + 128 * 104 = 64512 = the 384 * 168 launched.
@@ -146,6 +156,44 @@ struct Seq {
   }
 };
 
+// A sequence whose keys and values do not stay in L2 (kShareBytes) goes to the
+// workers in rounds first, as long as there are items for all of them: heads
+// 2x and 2x + 1 give one turn for each block m, blocks m of the first and
+// blocks - 1 - m of the second, so that causal turns cost the same, and worker w
+// takes turn w of a round. Neighbours then read a head's keys at the same time.
+// Returns the number of rounds; the items left over are dealt in runs. kRounds is
+// false in the kernel for calls in which no sequence can have rounds.
+template <bool kRounds>
+MLA_DEV int rounds_of(const AttnArgs& a, const Seq& s) {
+  if (!kRounds || s.blocks() < kShareBlocks || (long long)s.L * a.heads * kKeyBytes < kShareBytes) return 0;
+  return a.heads / 2 * s.blocks() / a.workers;
+}
+
+// What the rounds leave of a sequence: the items from block qb of head h on, in
+// the order head, block, without those of head `gap_h` from block `gap_qb` on.
+template <bool kRounds>
+struct Rest {
+  int h, qb, gap_h, gap_qb;
+  long long skipped, gap;  // units before the first of them, and of the gap
+  MLA_DEV Rest(const AttnArgs& a, const Seq& s) : h(0), qb(0), gap_h(-1), gap_qb(0), skipped(0), gap(0) {
+    const int rounds = rounds_of<kRounds>(a, s);
+    if (rounds == 0) return;
+    const int turns = rounds * a.workers, nb = s.blocks();
+    const long long per_head = s.units_before(nb, a.causal);
+    h = turns / nb * 2;
+    qb = turns % nb;
+    skipped = per_head * h + s.units_before(qb, a.causal);
+    if (qb > 0) {
+      gap_h = h + 1;
+      gap_qb = nb - qb;
+      gap = per_head - s.units_before(gap_qb, a.causal);
+    }
+  }
+  MLA_DEV long long units(const AttnArgs& a, const Seq& s) const {
+    return s.units_before(s.blocks(), a.causal) * a.heads - skipped - gap;
+  }
+};
+
 // A run's part of an item, as the producer hands it to the other warps.
 struct Item {
   int t0, t1;         // key tiles; t1 = 0: the run's end
@@ -159,16 +207,19 @@ struct Item {
 // Position of a run in the list of items. An item takes kItemUnits + tiles units
 // from `item` on; a run that begins or ends in the first kItemUnits begins with,
 // or ends before, the item's first tile.
+template <bool kRounds>
 struct Cursor {
   long long item, end;  // the item's first unit, the run's end
   long long quota;      // units of a run
   Seq s;
   int b, qb, h, t0, tiles;
   int group;            // heads of a group
+  int gap_h, gap_qb;    // of Rest
   MLA_DEV int t1() const { return (int)max(0ll, min((long long)tiles, end - item - kItemUnits)); }
   MLA_DEV bool more() const { return t0 < t1(); }
   // Heads of a group: about a run's number of items of this sequence.
   MLA_DEV static int group_heads(const AttnArgs& a, const Seq& s, long long quota) {
+    if (rounds_of<kRounds>(a, s) > 0) return 1;
     const long long per_head = s.units_before(s.blocks(), a.causal);
     return (int)min((long long)a.heads, max(1ll, quotient(quota * s.blocks() + per_head / 2, max(per_head, 1ll))));
   }
@@ -181,16 +232,19 @@ struct Cursor {
     }
     const int g0 = h - h % group;
     if (++h < min(g0 + group, a.heads)) return;
-    if (++qb < s.blocks()) {
+    if (++qb < (g0 == gap_h ? gap_qb : s.blocks())) {
       h = g0;
     } else {
       qb = 0;
       if (h >= a.heads) {  // the sequence's last group
-        h = 0;
         do {
-          ++b;
-          s.load(a, b);
-        } while (s.n == 0 && b + 1 < a.batch);
+          s.load(a, ++b);
+          const Rest<kRounds> r(a, s);
+          h = r.h;
+          qb = r.qb;
+          gap_h = r.gap_h;
+          gap_qb = r.gap_qb;
+        } while ((s.n == 0 || h == a.heads) && b + 1 < a.batch);
         group = group_heads(a, s, quota);
       }
     }
@@ -199,7 +253,8 @@ struct Cursor {
 };
 
 // Run `w`: called by a whole warp. Two passes over the sequences, 32 at a time.
-MLA_DEV void run_start(const AttnArgs& a, int w, Cursor* cur) {
+template <bool kRounds>
+MLA_DEV void run_start(const AttnArgs& a, int w, Cursor<kRounds>* cur) {
   const int lane = threadIdx.x & 31;
   long long total = 0, first_units = 0;
   Seq first{0, 0, 0, 0};  // this lane's sequence of the first 32
@@ -208,7 +263,7 @@ MLA_DEV void run_start(const AttnArgs& a, int w, Cursor* cur) {
   for (int b = lane; b < a.batch; b += 32) {
     Seq s;
     s.load(a, b);
-    const long long units = s.units_before(s.blocks(), a.causal) * a.heads;
+    const long long units = Rest<kRounds>(a, s).units(a, s);
     const int oq = __ldg(a.cu_q + b), ok = __ldg(a.cu_k + b);
     bad |= oq != s.q0 || ok != s.k0 || __ldg(a.cu_q + b + 1) != s.q0 + s.n || __ldg(a.cu_k + b + 1) != s.k0 + s.L;
     if (b == lane) {
@@ -229,6 +284,8 @@ MLA_DEV void run_start(const AttnArgs& a, int w, Cursor* cur) {
   cur->b = cur->qb = cur->h = cur->t0 = 0;
   cur->tiles = 0;
   cur->group = 1;
+  cur->gap_h = -1;
+  cur->gap_qb = 0;
   if (u >= total) return;
   long long before = 0;
 #pragma unroll 1
@@ -238,7 +295,7 @@ MLA_DEV void run_start(const AttnArgs& a, int w, Cursor* cur) {
     if (b0 > 0) {
       s = Seq{0, 0, 0, 0};
       if (b0 + lane < a.batch) s.load(a, b0 + lane);
-      own = s.units_before(s.blocks(), a.causal) * a.heads;
+      own = Rest<kRounds>(a, s).units(a, s);
     }
     long long incl = own;
 #pragma unroll
@@ -254,9 +311,14 @@ MLA_DEV void run_start(const AttnArgs& a, int w, Cursor* cur) {
       cur->s.n = __shfl_sync(~0u, s.n, src);
       cur->s.k0 = __shfl_sync(~0u, s.k0, src);
       cur->s.L = __shfl_sync(~0u, s.L, src);
-      cur->group = Cursor::group_heads(a, cur->s, quota);
+      cur->group = Cursor<kRounds>::group_heads(a, cur->s, quota);
       long long rest = u - before - __shfl_sync(~0u, incl - own, src);
       const long long per_head = cur->s.units_before(cur->s.blocks(), a.causal);
+      const Rest<kRounds> left(a, cur->s);
+      cur->gap_h = left.gap_h;
+      cur->gap_qb = left.gap_qb;
+      rest += left.skipped;
+      if (rest >= per_head * (left.gap_h + 1) - left.gap) rest += left.gap;
       const int g0 = (int)quotient(rest, per_head * cur->group) * cur->group;  // the group's first head
       const int heads = min(cur->group, a.heads - g0);
       rest -= per_head * g0;
@@ -340,6 +402,7 @@ MLA_DEV float max3(float a, float b, float c) {
   return d;
 }
 
+template <bool kRounds>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     mla_prefill_attention_kernel(const __grid_constant__ AttnMaps maps, const AttnArgs a) {
   extern __shared__ uint8_t smem_raw[];
@@ -405,9 +468,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
   }
   if (warp == 9) {
     // ------------------------------------------------------------ producer
-    Cursor cur;
+    Cursor<kRounds> cur;
     run_start(a, worker, &cur);
     if (elect_one()) {
+      // the rounds: sequence, half turn, number of half turns
+      Seq rs{0, 0, 0, 0};
+      int rb = kRounds ? -1 : a.batch, rk = 0, halves = 0;
       if (rank == 0) a.info[worker].pieces = 0;
       RingPos pk, pv;
       int nk = 0, nv = 0;           // items handed on, items of V begun
@@ -445,11 +511,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
           const int e = nk % kItems, b = nk & 1;
           if (!(ok = W.wait(&sh.item_free[e], ((nk / kItems) & 1) ^ 1))) break;
           Item& it = sh.item[e];
-          const int t1 = cur.t1(), r0 = cur.qb * kBlockQ;
+#pragma unroll 1
+          while (kRounds && rk == halves && rb < a.batch) {  // the next sequence with rounds
+            rk = halves = 0;
+            if (++rb < a.batch) {
+              rs.load(a, rb);
+              halves = 2 * rounds_of<kRounds>(a, rs);
+            }
+          }
+          const bool round = kRounds && rb < a.batch;
+          Seq s = cur.s;
+          int h = cur.h, qb = cur.qb, t1 = cur.t1(), tiles = cur.tiles;
           jk = cur.t0;
-          more = cur.more();
-          it = Item{jk, more ? t1 : 0, cur.s.q0 + r0, min(cur.s.n - r0, kBlockQ), cur.h, cur.s.L, cur.s.k0,
-                    cur.s.L - cur.s.n + r0, jk > 0 ? 0 : t1 < cur.tiles ? 1 : -1};
+          if (round) {
+            const int turn = (rk >> 1) * a.workers + worker, nb = rs.blocks();
+            s = rs;
+            h = turn / nb * 2 + (rk & 1);
+            qb = (rk & 1) ? nb - 1 - turn % nb : turn % nb;
+            jk = 0;
+            t1 = tiles = s.tiles((qb + 1) * kBlockQ, a.causal);
+            ++rk;
+          }
+          const int r0 = qb * kBlockQ;
+          more = jk < t1;
+          it = Item{jk, more ? t1 : 0, s.q0 + r0, min(s.n - r0, kBlockQ), h, s.L, s.k0, s.L - s.n + r0,
+                    jk > 0 ? 0 : t1 < tiles ? 1 : -1};
           mbar_arrive(smem_addr(&sh.item_full[e]));
           if (more) {
             k_end = t1;
@@ -460,7 +546,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
             mbar_arrive_expect_tx_cluster(leader(&sh.q_full[b]), kQBytes);
             tma_load_3d_pair(qbuf + b * kQBytes, &maps.q, 0, it.q + rank * kTile, 3 * it.h, leader(&sh.q_full[b]));
             ++nk;
-            cur.next(a);
+            if (!round) cur.next(a);
           }
         }
         if (more) {
@@ -873,8 +959,10 @@ int device_sms() {
   if (sms[dev] == 0) {
     int n = 0;
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        cudaFuncSetAttribute((const void*)mla_prefill_attention_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kAttnSmem) != cudaSuccess) {
+        cudaFuncSetAttribute((const void*)mla_prefill_attention_kernel<false>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, kAttnSmem) != cudaSuccess ||
+        cudaFuncSetAttribute((const void*)mla_prefill_attention_kernel<true>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, kAttnSmem) != cudaSuccess) {
       cudaGetLastError();
       return 0;
     }
@@ -954,7 +1042,8 @@ mla_status_t attention(const mlap_attention_desc_t* d, const void* q, const void
   a.workers = workers;
   a.scale = d->softmax_scale;
   a.scale_log2 = d->softmax_scale * 1.4426950408889634f;
-  if (launch_dependent(mla_prefill_attention_kernel, dim3(2 * workers), kAttnThreads, kAttnSmem, stream, maps, a) !=
+  const bool rounds = (long long)a.num_k * a.heads * kKeyBytes >= kShareBytes && a.num_q > (kShareBlocks - 1) * kBlockQ;
+  if (launch_dependent(rounds ? mla_prefill_attention_kernel<true> : mla_prefill_attention_kernel<false>, dim3(2 * workers), kAttnThreads, kAttnSmem, stream, maps, a) !=
       cudaSuccess)
     return MLA_ERR_CUDA;
   return launch_dependent(mla_prefill_merge_kernel, dim3(workers, kBlockQ / kMergeRows), 32 * kMergeRows, 0, stream, a) ==

@@ -552,3 +552,35 @@ def test_stream_argument_as_object_and_as_handle(dev):
         merged, mlse = merge_parts(out[None].contiguous(), lse[None].contiguous(), stream=stream)
         s.synchronize()
         assert torch.equal(merged, out) and torch.allclose(mlse, lse, atol=1e-6)
+
+
+# Keys and values of 64 MiB, from four blocks of queries on: such a sequence's
+# blocks go to the workers in rounds, two heads at a time, the rest in runs.
+ROUNDS = [
+    (33, [(1153, 4100), (0, 50), (700, 700), (2305, 4300)], True, 0),
+    (17, [(1025, 7800), (300, 9000), (1300, 7711)], False, 9),
+    (16, [(1024, 8192)], True, 2),          # one worker: nothing is left over
+    (16, [(900, 8192), (40, 60)], True, 6),
+    (128, [(1537, 1100), (1, 1)], True, 0),  # more queries than keys
+]
+
+
+@pytest.mark.parametrize("heads,seqs,causal,num_sms", ROUNDS)
+def test_attention_in_rounds(dev, heads, seqs, causal, num_sms):
+    """Every head of calls whose blocks share keys; heads repeat three heads' inputs."""
+    from mla_latent_kv_26_b200.prefill import prefill_attention
+
+    q, kv, pe, cu_q, cu_k = _attention_inputs(3, seqs, 101)
+    pick = [h % 3 for h in range(heads)]
+    err = torch.zeros(1, dtype=torch.int32, device=dev)
+    out = torch.full((q.shape[0], heads, 128), math.nan, dtype=torch.bfloat16, device=dev)
+    lse = torch.full((q.shape[0], heads), math.nan, device=dev)
+    prefill_attention(q.to(dev)[:, pick], kv.to(dev)[:, pick], pe.to(dev), cu_q.to(dev), cu_k.to(dev), causal=causal,
+                      num_sms=num_sms, out=out, lse=lse, error_word=err)
+    assert int(err.item()) == 0
+    out, lse = out.cpu(), lse.cpu()
+    for first in range(0, heads, 3):
+        heads3 = list(range(first, min(first + 3, heads)))
+        some = [h % 3 for h in heads3]
+        _check_attention(out[:, heads3], lse[:, heads3], q[:, some], kv[:, some], pe, cu_q, cu_k, causal,
+                         oracle.DEFAULT_SOFTMAX_SCALE, where=f"heads {heads3}")
