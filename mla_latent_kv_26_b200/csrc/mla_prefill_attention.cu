@@ -25,7 +25,9 @@
 // of 2.35; 16 heads, 16384 new tokens: 0.97 ms instead of 1.12. With two or three
 // blocks the keys are read too few times for that to pay: 600 queries over 7000
 // keys, 128 heads, 371 us in rounds, 357 in runs; with four (1024 over 8192)
-// within 1 % not causal, 484 us instead of 501 causal.
+// within 1 % not causal, 484 us instead of 501 causal. (A kernel that knows
+// rounds, on calls whose sequences have none: 400 prompts of 300 tokens 1.013 ms
+// instead of 0.993; calls too small for any get the one that does not.)
 //
 // A CTA pair (cta_group::2) works on a block: S = Q K^T and O += P V with M 256,
 // 128 rows in each CTA. Each CTA loads half of every key tile (64 keys of K,
@@ -215,6 +217,7 @@ struct Cursor {
   int b, qb, h, t0, tiles;
   int group;            // heads of a group
   int gap_h, gap_qb;    // of Rest
+  int round_b, round_end;  // from the first sequence with rounds to behind the last
   MLA_DEV int t1() const { return (int)max(0ll, min((long long)tiles, end - item - kItemUnits)); }
   MLA_DEV bool more() const { return t0 < t1(); }
   // Heads of a group: about a run's number of items of this sequence.
@@ -258,12 +261,18 @@ MLA_DEV void run_start(const AttnArgs& a, int w, Cursor<kRounds>* cur) {
   const int lane = threadIdx.x & 31;
   long long total = 0, first_units = 0;
   Seq first{0, 0, 0, 0};  // this lane's sequence of the first 32
+  int round_b = a.batch, round_end = 0;
   bool bad = false;
 #pragma unroll 1
   for (int b = lane; b < a.batch; b += 32) {
     Seq s;
     s.load(a, b);
-    const long long units = Rest<kRounds>(a, s).units(a, s);
+    const Rest<kRounds> left(a, s);
+    const long long units = left.units(a, s);
+    if (left.skipped > 0) {
+      round_b = min(round_b, b);
+      round_end = b + 1;
+    }
     const int oq = __ldg(a.cu_q + b), ok = __ldg(a.cu_k + b);
     bad |= oq != s.q0 || ok != s.k0 || __ldg(a.cu_q + b + 1) != s.q0 + s.n || __ldg(a.cu_k + b + 1) != s.k0 + s.L;
     if (b == lane) {
@@ -284,6 +293,8 @@ MLA_DEV void run_start(const AttnArgs& a, int w, Cursor<kRounds>* cur) {
   cur->b = cur->qb = cur->h = cur->t0 = 0;
   cur->tiles = 0;
   cur->group = 1;
+  cur->round_b = __reduce_min_sync(~0u, round_b);
+  cur->round_end = __reduce_max_sync(~0u, round_end);
   cur->gap_h = -1;
   cur->gap_qb = 0;
   if (u >= total) return;
@@ -366,6 +377,7 @@ struct AttnShared {
   uint64_t item_full[kItems], item_free[kItems];  // entry of item[], read by all other warps
   Item item[kItems];
   PendingRows pending[8];
+  Cursor<true> run;                            // the producer's run while it is in rounds
   float m[2][kTile];                           // reference maximum after tile n, entry n % 2
   float fin_m[2][2][kTile], fin_l[2][2][kTile];  // [item % 2][warpgroup]
   uint32_t tmem;
@@ -471,9 +483,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     Cursor<kRounds> cur;
     run_start(a, worker, &cur);
     if (elect_one()) {
-      // the rounds: sequence, half turn, number of half turns
-      Seq rs{0, 0, 0, 0};
-      int rb = kRounds ? -1 : a.batch, rk = 0, halves = 0;
+      // Rounds come first: the cursor is at one of their items, an item's end its
+      // run's end, and the run's start waits in shared memory.
+      int rb = cur.round_b - 1, rk = 0, halves = 0;  // sequence, half turn, half turns
+      const int round_end = cur.round_end;
+      bool in_rounds = kRounds && cur.round_b < round_end;
+      const auto next_turn = [&]() {
+        if constexpr (kRounds) {
+#pragma unroll 1
+          while (rk == halves) {
+            if (++rb >= round_end) {
+              cur = sh.run;
+              return false;
+            }
+            cur.s.load(a, rb);
+            halves = 2 * rounds_of<kRounds>(a, cur.s);
+            rk = 0;
+          }
+          const int turn = (rk >> 1) * a.workers + worker, nb = cur.s.blocks();
+          cur.h = turn / nb * 2 + (rk & 1);
+          cur.qb = (rk & 1) ? nb - 1 - turn % nb : turn % nb;
+          cur.tiles = cur.s.tiles((cur.qb + 1) * kBlockQ, a.causal);
+          cur.t0 = 0;
+          cur.item = 0;
+          cur.end = cur.tiles + kItemUnits;
+          ++rk;
+        }
+        return true;
+      };
+      if constexpr (kRounds) {
+        if (in_rounds) {
+          sh.run = cur;
+          in_rounds = next_turn();
+        }
+      }
       if (rank == 0) a.info[worker].pieces = 0;
       RingPos pk, pv;
       int nk = 0, nv = 0;           // items handed on, items of V begun
@@ -511,31 +554,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
           const int e = nk % kItems, b = nk & 1;
           if (!(ok = W.wait(&sh.item_free[e], ((nk / kItems) & 1) ^ 1))) break;
           Item& it = sh.item[e];
-#pragma unroll 1
-          while (kRounds && rk == halves && rb < a.batch) {  // the next sequence with rounds
-            rk = halves = 0;
-            if (++rb < a.batch) {
-              rs.load(a, rb);
-              halves = 2 * rounds_of<kRounds>(a, rs);
-            }
-          }
-          const bool round = kRounds && rb < a.batch;
-          Seq s = cur.s;
-          int h = cur.h, qb = cur.qb, t1 = cur.t1(), tiles = cur.tiles;
+          const int t1 = cur.t1(), r0 = cur.qb * kBlockQ;
           jk = cur.t0;
-          if (round) {
-            const int turn = (rk >> 1) * a.workers + worker, nb = rs.blocks();
-            s = rs;
-            h = turn / nb * 2 + (rk & 1);
-            qb = (rk & 1) ? nb - 1 - turn % nb : turn % nb;
-            jk = 0;
-            t1 = tiles = s.tiles((qb + 1) * kBlockQ, a.causal);
-            ++rk;
-          }
-          const int r0 = qb * kBlockQ;
-          more = jk < t1;
-          it = Item{jk, more ? t1 : 0, s.q0 + r0, min(s.n - r0, kBlockQ), h, s.L, s.k0, s.L - s.n + r0,
-                    jk > 0 ? 0 : t1 < tiles ? 1 : -1};
+          more = cur.more();
+          it = Item{jk, more ? t1 : 0, cur.s.q0 + r0, min(cur.s.n - r0, kBlockQ), cur.h, cur.s.L, cur.s.k0,
+                    cur.s.L - cur.s.n + r0, jk > 0 ? 0 : t1 < cur.tiles ? 1 : -1};
           mbar_arrive(smem_addr(&sh.item_full[e]));
           if (more) {
             k_end = t1;
@@ -546,7 +569,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
             mbar_arrive_expect_tx_cluster(leader(&sh.q_full[b]), kQBytes);
             tma_load_3d_pair(qbuf + b * kQBytes, &maps.q, 0, it.q + rank * kTile, 3 * it.h, leader(&sh.q_full[b]));
             ++nk;
-            if (!round) cur.next(a);
+            if (in_rounds) in_rounds = next_turn();
+            else cur.next(a);
           }
         }
         if (more) {
@@ -1042,7 +1066,10 @@ mla_status_t attention(const mlap_attention_desc_t* d, const void* q, const void
   a.workers = workers;
   a.scale = d->softmax_scale;
   a.scale_log2 = d->softmax_scale * 1.4426950408889634f;
-  const bool rounds = (long long)a.num_k * a.heads * kKeyBytes >= kShareBytes && a.num_q > (kShareBlocks - 1) * kBlockQ;
+  // whether rounds_of can be above 0 for a sequence of these rows
+  const int blocks = (a.num_q + kBlockQ - 1) / kBlockQ;
+  const bool rounds = (long long)a.num_k * a.heads * kKeyBytes >= kShareBytes && blocks >= kShareBlocks &&
+                      (long long)(a.heads / 2) * blocks >= workers;
   if (launch_dependent(rounds ? mla_prefill_attention_kernel<true> : mla_prefill_attention_kernel<false>, dim3(2 * workers), kAttnThreads, kAttnSmem, stream, maps, a) !=
       cudaSuccess)
     return MLA_ERR_CUDA;

@@ -584,3 +584,35 @@ def test_attention_in_rounds(dev, heads, seqs, causal, num_sms):
         some = [h % 3 for h in heads3]
         _check_attention(out[:, heads3], lse[:, heads3], q[:, some], kv[:, some], pe, cu_q, cu_k, causal,
                          oracle.DEFAULT_SOFTMAX_SCALE, where=f"heads {heads3}")
+
+
+def test_default_stream_by_its_handle(dev):
+    """Handle 0 is the default stream, whatever the current one is."""
+    from mla_latent_kv_26_b200.prefill import cache_read, expand_kv, prefill_attention
+
+    cache, bt, q, w, cu_q, cu_k = _chunk([(60, 150)], 2, 93, False)
+    g = [t.to(dev) for t in (cache, bt, q, w, cu_q, cu_k)]
+    torch.cuda.synchronize(dev)
+    with torch.cuda.stream(torch.cuda.Stream(dev)):
+        rows = cache_read(g[0], g[1], g[5], num_rows=150, stream=0)
+        kv = expand_kv(rows, g[3], stream=0)
+        out, lse = prefill_attention(g[2], kv, rows[:, 512:], g[4], g[5], stream=0)
+    torch.cuda.default_stream(dev).synchronize()
+    _check_chunk(out, lse, cache, bt, q, w, cu_q, cu_k)
+
+
+def test_rounds_between_many_short_sequences(dev):
+    """Sequences with rounds at both ends of a list longer than a warp scans at once."""
+    from mla_latent_kv_26_b200.prefill import prefill_attention
+
+    seqs = [(1030, 8200)] + [(i % 4, 3 * i) for i in range(60)] + [(0, 0), (1300, 8192), (7, 9)]
+    q, kv, pe, cu_q, cu_k = _attention_inputs(2, seqs, 102)
+    pick = [h % 2 for h in range(16)]
+    for num_sms in (0, 14):
+        err = torch.zeros(1, dtype=torch.int32, device=dev)
+        out, lse = prefill_attention(q.to(dev)[:, pick], kv.to(dev)[:, pick], pe.to(dev), cu_q.to(dev), cu_k.to(dev),
+                                     num_sms=num_sms, error_word=err)
+        assert int(err.item()) == 0
+        for h in range(0, 16, 2):
+            _check_attention(out[:, h:h + 2], lse[:, h:h + 2], q, kv, pe, cu_q, cu_k, True,
+                             oracle.DEFAULT_SOFTMAX_SCALE, where=f"heads {h}, {h + 1}, num_sms {num_sms}")
