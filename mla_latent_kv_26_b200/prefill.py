@@ -30,6 +30,7 @@ import torch
 from . import binding as B
 
 _BF16, _I32, _U8, _F32 = torch.bfloat16, torch.int32, torch.uint8, torch.float32
+_INT_MAX = 0x7fffffff
 _HERE = contextlib.nullcontext()
 
 
@@ -55,8 +56,8 @@ def _row_stride(name, t, dev, width, exact):
         raise ValueError(f"{name}: rows of {cols} values, {'' if exact else 'at least '}{width} needed")
     s0, s1 = t.stride()
     stride = s0 if rows > 1 else (cols + 7) // 8 * 8  # the stride of a single row is never used
-    if (rows and s1 != 1) or stride < width or stride % 8 or t.data_ptr() % 16:
-        raise ValueError(f"{name}: rows must be dense, 16-byte aligned and a multiple of 8 elements apart")
+    if (rows and s1 != 1) or stride < width or stride % 8 or stride > _INT_MAX or t.data_ptr() % 16:
+        raise ValueError(f"{name}: rows must be dense, 16-byte aligned and a multiple of 8 (below 2^31) elements apart")
     return stride
 
 
@@ -79,8 +80,8 @@ def _allocate(stream, dev, *shape, dtype):
     """A tensor that belongs to the stream the kernels are launched on."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=dev)
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=dev)
+    if isinstance(stream, int):  # 0: the default stream, which is not an external one
+        stream = torch.cuda.ExternalStream(stream, device=dev) if stream else torch.cuda.default_stream(dev)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=dev)
 
@@ -94,8 +95,8 @@ def _check_cache(kv_cache, block_table, row_offsets, starts, dev):
         raise ValueError("kv_cache must be [pages, 64, 576] bf16 or [pages, 64, 656] uint8, "
                          "block_table [batch, max_pages_per_seq]")
     batch, width = block_table.shape
-    if kv_cache.shape[0] == 0 or width == 0:
-        raise ValueError("kv_cache, block_table: empty")
+    if kv_cache.shape[0] == 0 or not 0 < width <= _INT_MAX:
+        raise ValueError("kv_cache, block_table: empty, or more than 2^31 - 1 pages per sequence")
     _check("kv_cache", kv_cache, _U8 if fp8 else _BF16, None, dev)
     _check("block_table", block_table, _I32, None, dev)
     _check("row_offsets", row_offsets, _I32, (batch + 1,), dev)
@@ -136,7 +137,7 @@ def cache_read(kv_cache: torch.Tensor, block_table: torch.Tensor, row_offsets: t
         if num_rows is None:
             raise ValueError("cache_read needs out or num_rows")
         out = _allocate(stream, dev, num_rows, 576, dtype=_BF16)
-    elif out.dim() != 2:
+    elif not isinstance(out, torch.Tensor) or out.dim() != 2:
         raise ValueError("out: need a [rows, 576] tensor")
     _check("out", out, _BF16, (out.shape[0], 576), dev)
     with _on(dev):

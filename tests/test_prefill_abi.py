@@ -189,3 +189,12 @@ def test_wrappers_refuse_wrong_shapes_types_and_strides(libmla):
             prefill.cache_read(cache, table, off, **dict(dict(num_rows=4), **kw))
     with pytest.raises(ValueError):
         prefill.cache_read(_on(d, (2, 64, 576)), table, off)
+
+
+@pytest.mark.gpu
+def test_cache_read_refuses_an_out_that_is_no_tensor(libmla):
+    from mla_latent_kv_26_b200 import prefill
+
+    off = torch.tensor([0, 4], dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        prefill.cache_read(_on("cuda", (2, 64, 576)), off[None].contiguous(), off, out=[0.0] * 4)
