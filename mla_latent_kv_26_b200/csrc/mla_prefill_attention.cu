@@ -25,7 +25,9 @@
 // of 2.35; 16 heads, 16384 new tokens: 0.97 ms instead of 1.12. With two or three
 // blocks the keys are read too few times for that to pay: 600 queries over 7000
 // keys, 128 heads, 371 us in rounds, 357 in runs; with four (1024 over 8192)
-// within 1 % not causal, 484 us instead of 501 causal. (A kernel that knows
+// within 1 % not causal, 484 us instead of 501 causal. Below 64 MiB of keys and
+// values rounds cost 2 to 3 % (4096 new tokens, 16 heads: 85 us for 83), from
+// there on they gain (2048, 64 heads: 94 us for 96). (A kernel that knows
 // rounds, on calls whose sequences have none: 400 prompts of 300 tokens 1.013 ms
 // instead of 0.993; calls too small for any get the one that does not.)
 //
