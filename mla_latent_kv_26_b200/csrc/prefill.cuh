@@ -56,8 +56,7 @@ struct Waiter {
 };
 
 // a / b for a >= 0, b > 0: one 32-bit division where both fit, else bit by bit
-// (a call that long runs for a minute). The compiler's 64-bit division, inlined
-// wherever one is needed, made up a seventh of the attention kernel's code.
+// (a call that long runs for a minute).
 MLA_DEV long long quotient(long long a, long long b) {
   if (((unsigned long long)a | (unsigned long long)b) >> 32 == 0) return (uint32_t)a / (uint32_t)b;
   unsigned long long q = 0, r = 0;
