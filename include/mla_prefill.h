@@ -112,11 +112,12 @@ MLA_API mla_status_t mlap_expand_kv(const mlap_expand_desc_t* desc, const void* 
  *   lse  = ln sum_{t in T} exp(s_t)
  *   out  = sum_{t in T} exp(s_t - lse) * kv[t,h,128:256]
  *
- * A row with no visible key gets out = 0, lse = -inf. Without `causal` the call
- * computes one part of a longer context; mla_merge (d_latent = 128) joins the
- * parts. Rows of kv and k_pe that no sequence owns may hold anything; a
- * sequence's own rows must be finite (a masked value still enters the tensor
- * cores' products with weight 0).
+ * A row with no visible key gets out = 0, lse = -inf. A NaN or an infinity in
+ * q[i,h] makes out and lse of that query and head NaN if it sees a key, and touches
+ * no other row. Without `causal` the call computes one part of a longer context;
+ * mla_merge (d_latent = 128) joins the parts. Rows of kv and k_pe that no sequence
+ * owns may hold anything; a sequence's own rows must be finite (a masked value
+ * still enters the tensor cores' products with weight 0).
  *
  *   q      bf16 [num_q, H, 192]  (q_nope[128] || q_pe[64], q_pe rotated)
  *   kv     bf16 [num_k, H, 256]  (mlap_expand_kv)

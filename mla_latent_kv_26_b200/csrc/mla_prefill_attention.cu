@@ -6,6 +6,10 @@
 //   s_t = scale * q . k_t,  p_t = exp(s_t - m),  l = sum_t p_t,  o = sum_t p_t v_t
 //   out = o / l,  lse = m + ln l
 // one pass over the keys; when m grows, o and l are scaled by exp(m_old - m).
+// A row without a key has l = 0: out = 0, lse = -inf. A NaN or an infinity in q
+// makes l NaN, or 0 where every score is -inf: out = NaN, lse = NaN. Hence l is
+// compared with 0 and never tested for being above it, and a row with l = 0 is
+// taken for one without keys only if none is visible to it (`blind`).
 //
 // Work. An item is (sequence, block of 256 queries, head); its units are its
 // visible 128-key tiles, and kItemUnits more for what an item costs beside its
@@ -100,9 +104,10 @@ constexpr int kItemUnits = 3;              // cost of an item beside its tiles, 
 constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;
 
 // What the merge kernel needs about the item that run w starts and does not
-// finish: the number of runs it spans (0: none), its first query row, rows, head.
+// finish: the number of runs it spans (0: none), its first query row, rows, head,
+// and how many of its rows, the first ones, see no key.
 struct SplitInfo {
-  int32_t pieces, row, rows, head;
+  int32_t pieces, row, rows, head, blind;
 };
 
 struct AttnArgs {
@@ -206,6 +211,8 @@ struct Item {
   int L, k0;          // the sequence's keys, the first one's row
   int sees;           // keys that the query before the block's first sees, when causal
   int part;           // all of the item's keys: -1; else the slot of its partials (0, 1)
+  // rows of the block, its first ones, that see no key
+  MLA_DEV int blind(int causal) const { return causal ? min(max(-sees, 0), kBlockQ) : L > 0 ? 0 : kBlockQ; }
 };
 
 // Position of a run in the list of items. An item takes kItemUnits + tiles units
@@ -358,6 +365,7 @@ MLA_DEV void run_start(const AttnArgs& a, int w, Cursor<kRounds>* cur) {
 // An item whose rows a softmax warp has still to write.
 struct PendingRows {
   int q, rows, h;     // output row of the warp's lane 0, lanes with a row, head
+  int blind;          // lanes, the first ones, whose row sees no key
   int live, whole;    // rows of this CTA at all; all of the item's keys (not a part)
   long long part;     // else: row of the partials
 };
@@ -566,7 +574,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
             k_end = t1;
             if (rank == 0 && it.part == 1)  // the item goes on in the following runs
               a.info[worker] = SplitInfo{
-                  (int)(quotient(cur.item + kItemUnits + cur.tiles - 1, cur.quota) - worker) + 1, it.q, it.rows, it.h};
+                  (int)(quotient(cur.item + kItemUnits + cur.tiles - 1, cur.quota) - worker) + 1, it.q, it.rows, it.h,
+                  it.blind(a.causal)};
             if (!(ok = W.wait(&sh.q_empty[b], ((nk >> 1) & 1) ^ 1))) break;
             mbar_arrive_expect_tx_cluster(leader(&sh.q_full[b]), kQBytes);
             tma_load_3d_pair(qbuf + b * kQBytes, &maps.q, 0, it.q + rank * kTile, 3 * it.h, leader(&sh.q_full[b]));
@@ -736,10 +745,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
       const float m0 = sh.fin_m[nf & 1][0][row], m1 = sh.fin_m[nf & 1][1][row], mm = fmaxf(m0, m1);
       const float l0 = sh.fin_l[nf & 1][0][row], l1 = sh.fin_l[nf & 1][1][row];
       ++nf;
-      float l = l0 > 0.f ? l0 * ex2((m0 - mm) * a.scale_log2) : 0.f;
-      if (l1 > 0.f) l += l1 * ex2((m1 - mm) * a.scale_log2);
-      const float inv = l > 0.f ? 1.f / l : 0.f;       // a row without keys: its products are all 0 * v
-      const float lse = l > 0.f ? mm * a.scale + logf(l) : -INFINITY;
+      float l = l0 != 0.f ? l0 * ex2((m0 - mm) * a.scale_log2) : 0.f;
+      if (l1 != 0.f) l += l1 * ex2((m1 - mm) * a.scale_log2);
+      // l = 0: no keys (the products are all 0 * v), or nothing but -inf scores; of
+      // a part only the merge knows which, it writes (0, -inf)
+      const float none = pr.whole && lane >= pr.blind ? NAN : 0.f;
+      const float inv = l != 0.f ? 1.f / l : none;
+      const float lse = l != 0.f ? mm * a.scale + logf(l) : none - INFINITY;
       if (valid) {
 #pragma unroll
         for (int x = 0; x < 64; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * inv);
@@ -897,7 +909,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
       }
       if (lane == 0) {
         const int r0 = kTile * rank + quad * 32;
-        sh.pending[warp] = PendingRows{it.q + r0, it.rows - r0, it.h, live, it.part < 0,
+        sh.pending[warp] = PendingRows{it.q + r0, it.rows - r0, it.h, it.blind(a.causal) - r0, live, it.part < 0,
                                        (2ll * worker + it.part) * kBlockQ + r0};
         mbar_arrive(smem_addr(&sh.item_free[ne % kItems]));
       }
@@ -944,7 +956,7 @@ __global__ void __launch_bounds__(32 * kMergeRows) mla_prefill_merge_kernel(cons
       const float f = __shfl_sync(~0u, weight, p);
       const float4 v = reinterpret_cast<const float4*>(a.part_o + slot(p0 + p) * 128)[lane];
       sum += f;
-      if (f > 0.f) {  // a part without keys counts for nothing, whatever its rows hold
+      if (f != 0.f) {  // a part without keys counts for nothing, whatever its rows hold
         acc.x = fmaf(f, v.x, acc.x);
         acc.y = fmaf(f, v.y, acc.y);
         acc.z = fmaf(f, v.z, acc.z);
@@ -952,11 +964,12 @@ __global__ void __launch_bounds__(32 * kMergeRows) mla_prefill_merge_kernel(cons
       }
     }
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float none = row >= it.blind ? NAN : 0.f;  // keys, and nothing but -inf scores: NaN
+  const float inv = sum != 0.f ? 1.f / sum : none;
   const size_t r = (size_t)(it.row + row) * a.heads + it.head;
   reinterpret_cast<uint2*>(a.out + r * 128)[lane] =
       make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-  if (lane == 0) a.lse[r] = sum > 0.f ? m + logf(sum) : -INFINITY;
+  if (lane == 0) a.lse[r] = sum != 0.f ? m + logf(sum) : none - INFINITY;
 }
 
 mla_status_t check_attention(const mlap_attention_desc_t* d) {

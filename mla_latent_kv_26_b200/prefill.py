@@ -188,8 +188,9 @@ def prefill_attention(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, cu_
     ``cu_q``, ``cu_k`` int32 [batch + 1]. Causal: a sequence's queries are its
     last positions; otherwise every query sees every key of its sequence (one
     part of a context, merged with others by :func:`merge_parts`). A row
-    without keys gets zeros and -inf; rows that no sequence owns are left as
-    they were. ``workspace`` (uint8, :func:`attention_workspace_bytes`) is
+    without keys gets zeros and -inf, a NaN or an infinity in a row of ``q`` NaN
+    for its head (``kv`` and ``k_pe`` must be finite in the rows that a sequence
+    owns); rows that no sequence owns are left as they were. ``workspace`` (uint8, :func:`attention_workspace_bytes`) is
     allocated when not given; calls that may run at the same time, and graphs
     that may replay at the same time, need one each."""
     dev = _device("q", q)
