@@ -171,7 +171,8 @@ MLA_API mla_status_t mla_get_error(const void* plan, uint32_t* error_bits, mla_s
  *   lse = ln sum_i exp(lse_i),   out = sum_i exp(lse_i - lse) * out_i
  *
  * parts with lse_i = -inf (no visible token in that shard) weigh nothing;
- * a row empty in every part gets out = 0, lse = -inf.
+ * a row empty in every part gets out = 0, lse = -inf; a row with a NaN lse_i
+ * gets NaN in out and lse.
  * Width D = d_latent: 512 for mla_decode outputs, 128 for the per-head outputs
  * of mlap_attention over parts of a context (mla_prefill.h).
  *   part_out  bf16 [parts, rows, D] (each part's output, rows = B * Sq * H)

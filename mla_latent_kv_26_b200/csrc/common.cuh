@@ -120,9 +120,9 @@ struct CombineArgs {
 };
 
 struct MergeArgs {
-  const __nv_bfloat16* part_out;  // [parts, rows, 512]
+  const __nv_bfloat16* part_out;  // [parts, rows, width], width 512 or 128
   const float* part_lse;          // [parts, rows]
-  __nv_bfloat16* out;             // [rows, 512]
+  __nv_bfloat16* out;             // [rows, width]
   float* lse;                     // [rows]
   int parts;
   long long rows;

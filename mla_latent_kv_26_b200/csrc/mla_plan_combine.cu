@@ -160,7 +160,8 @@ __global__ void __launch_bounds__(256) mla_combine_kernel(CombineArgs a) {
 // of a warp hold 8 columns each, so that a 512-wide row takes a warp twice
 // and a 128-wide row half a warp once (rows of part_out and out are kWidth wide).
 // lse = M + ln sum_i exp(lse_i - M), out = sum_i exp(lse_i - lse) * out_i;
-// parts with lse_i = -inf weigh nothing; all empty: out = 0, lse = -inf.
+// parts with lse_i = -inf weigh nothing; all empty: out = 0, lse = -inf. A NaN
+// lse_i goes through its weight into the sum, out and lse (fmaxf passes it by).
 template <int kWidth>
 __global__ void __launch_bounds__(256) mla_merge_kernel(MergeArgs a) {
   constexpr int kLanes = kWidth / 8 < 32 ? kWidth / 8 : 32;  // lanes of a row
@@ -174,27 +175,25 @@ __global__ void __launch_bounds__(256) mla_merge_kernel(MergeArgs a) {
 #pragma unroll
   for (int j = 0; j < 8 * kChunks; ++j) acc[j] = 0.f;
   float sum = 0.f;
-  if (m != -INFINITY) {
-    for (int i = 0; i < a.parts; ++i) {
-      const float l = a.part_lse[(size_t)i * a.rows + row];
-      if (l == -INFINITY) continue;
-      const float e = expf(l - m);
-      sum += e;
-      const uint4* src = reinterpret_cast<const uint4*>(a.part_out + ((size_t)i * a.rows + row) * kWidth);
+  for (int i = 0; i < a.parts; ++i) {
+    const float l = a.part_lse[(size_t)i * a.rows + row];
+    if (l == -INFINITY) continue;
+    const float e = expf(l - m);
+    sum += e;
+    const uint4* src = reinterpret_cast<const uint4*>(a.part_out + ((size_t)i * a.rows + row) * kWidth);
 #pragma unroll
-      for (int h = 0; h < kChunks; ++h) {
-        const uint4 v = src[lane + 32 * h];
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    for (int h = 0; h < kChunks; ++h) {
+      const uint4 v = src[lane + 32 * h];
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[u]));
-          acc[8 * h + 2 * u] += e * f.x;
-          acc[8 * h + 2 * u + 1] += e * f.y;
-        }
+      for (int u = 0; u < 4; ++u) {
+        const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[u]));
+        acc[8 * h + 2 * u] += e * f.x;
+        acc[8 * h + 2 * u + 1] += e * f.y;
       }
     }
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = sum != 0.f ? 1.f / sum : 0.f;
   uint4* dst = reinterpret_cast<uint4*>(a.out + (size_t)row * kWidth);
 #pragma unroll
   for (int h = 0; h < kChunks; ++h) {
@@ -206,7 +205,7 @@ __global__ void __launch_bounds__(256) mla_merge_kernel(MergeArgs a) {
     }
     dst[lane + 32 * h] = make_uint4(w[0], w[1], w[2], w[3]);
   }
-  if (lane == 0) a.lse[row] = sum > 0.f ? m + logf(sum) : -INFINITY;
+  if (lane == 0) a.lse[row] = sum != 0.f ? m + logf(sum) : -INFINITY;
 }
 
 cudaError_t launch_merge(const MergeArgs& args, int width, cudaStream_t stream) {

@@ -231,7 +231,8 @@ def prefill_attention(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, cu_
 def merge_parts(part_out: torch.Tensor, part_lse: torch.Tensor, *, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Merge of attention results over disjoint parts of each row's keys:
     ``part_out`` [parts, ..., 128] bf16, ``part_lse`` [parts, ...] float32
-    (``mla_merge``)."""
+    (``mla_merge``). A part with lse -inf weighs nothing, a NaN lse makes its
+    row NaN."""
     dev = _device("part_out", part_out)
     _check("part_out", part_out, torch.bfloat16, None, dev)
     _check("part_lse", part_lse, torch.float32, tuple(part_out.shape[:-1]), dev)
