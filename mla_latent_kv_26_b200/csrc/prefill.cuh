@@ -84,7 +84,8 @@ MLA_DEV int ragged_range(const int32_t* offsets, int b, int rows, int* first) {
 
 // Launch with programmatic stream serialization: the kernel may be set up while
 // the one before it in the stream still runs, and reads and writes global memory
-// only behind grid_dependency_wait().
+// only behind grid_dependency_wait(). A refused launch is reported once: the
+// runtime's last error, which a later call would find, is cleared.
 template <typename Kernel, typename... Args>
 inline cudaError_t launch_dependent(Kernel kernel, dim3 grid, int threads, int smem, cudaStream_t stream,
                                     const Args&... args) {
@@ -98,7 +99,9 @@ inline cudaError_t launch_dependent(Kernel kernel, dim3 grid, int threads, int s
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  if (e != cudaSuccess) cudaGetLastError();
+  return e;
 }
 
 }  // namespace prefill
