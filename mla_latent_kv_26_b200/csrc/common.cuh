@@ -119,6 +119,13 @@ struct CombineArgs {
   int q_len, heads;
 };
 
+// The outcome of a runtime call, its error reported this once: the runtime's last
+// error, which the next call's cudaGetLastError() would find, is cleared.
+inline cudaError_t reported(cudaError_t e) {
+  if (e != cudaSuccess) cudaGetLastError();
+  return e;
+}
+
 struct MergeArgs {
   const __nv_bfloat16* part_out;  // [parts, rows, width], width 512 or 128
   const float* part_lse;          // [parts, rows]

@@ -305,9 +305,9 @@ mla_status_t mla_combine(const mla_decode_desc_t* desc, void* plan, const void* 
 
 mla_status_t mla_get_error(const void* plan, uint32_t* error_bits, mla_stream_t stream) {
   if (!plan) return MLA_ERR_INVALID_ARG;
-  if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) return MLA_ERR_CUDA;
+  if (reported(cudaStreamSynchronize((cudaStream_t)stream)) != cudaSuccess) return MLA_ERR_CUDA;
   uint32_t bits = 0;
-  if (cudaMemcpy(&bits, plan, sizeof(bits), cudaMemcpyDeviceToHost) != cudaSuccess) return MLA_ERR_CUDA;
+  if (reported(cudaMemcpy(&bits, plan, sizeof(bits), cudaMemcpyDeviceToHost)) != cudaSuccess) return MLA_ERR_CUDA;
   if (error_bits) *error_bits = bits;
   if (bits & kErrTimeout) return MLA_ERR_DEVICE_TIMEOUT;
   if (bits) return MLA_ERR_DEVICE_BOUNDS;

@@ -1142,8 +1142,8 @@ cudaError_t launch_decode(const CacheMaps& maps, const DecodeArgs& args, int wor
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return fp8 ? cudaLaunchKernelEx(&cfg, dec::mla_decode_kernel<true>, maps, args)
-             : cudaLaunchKernelEx(&cfg, dec::mla_decode_kernel<false>, maps, args);
+  return reported(fp8 ? cudaLaunchKernelEx(&cfg, dec::mla_decode_kernel<true>, maps, args)
+                      : cudaLaunchKernelEx(&cfg, dec::mla_decode_kernel<false>, maps, args));
 }
 
 }  // namespace mla

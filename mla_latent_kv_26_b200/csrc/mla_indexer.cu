@@ -651,5 +651,5 @@ extern "C" MLA_API mla_status_t mla_topk(const mla_topk_desc_t* desc, const floa
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, idx::mla_topk_kernel, a) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+  return reported(cudaLaunchKernelEx(&cfg, idx::mla_topk_kernel, a)) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }

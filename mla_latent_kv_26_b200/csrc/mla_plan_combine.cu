@@ -233,7 +233,7 @@ cudaError_t launch_combine(const CombineArgs& args, int tasks, cudaStream_t stre
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, mla_combine_kernel, args);
+  return reported(cudaLaunchKernelEx(&cfg, mla_combine_kernel, args));
 }
 
 }  // namespace mla

@@ -84,8 +84,7 @@ MLA_DEV int ragged_range(const int32_t* offsets, int b, int rows, int* first) {
 
 // Launch with programmatic stream serialization: the kernel may be set up while
 // the one before it in the stream still runs, and reads and writes global memory
-// only behind grid_dependency_wait(). A refused launch is reported once: the
-// runtime's last error, which a later call would find, is cleared.
+// only behind grid_dependency_wait().
 template <typename Kernel, typename... Args>
 inline cudaError_t launch_dependent(Kernel kernel, dim3 grid, int threads, int smem, cudaStream_t stream,
                                     const Args&... args) {
@@ -99,9 +98,7 @@ inline cudaError_t launch_dependent(Kernel kernel, dim3 grid, int threads, int s
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
-  if (e != cudaSuccess) cudaGetLastError();
-  return e;
+  return reported(cudaLaunchKernelEx(&cfg, kernel, args...));
 }
 
 }  // namespace prefill

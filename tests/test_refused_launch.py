@@ -58,3 +58,34 @@ def test_refused_launch_is_not_reported_again(dev, libmla, call):
             st = libmla.mlap_attention(ad, x, x, x, i32, i32, x, x, ws, ws.numel(), None, s)
     assert st == libmla.MLA_ERR_CUDA
     _merge_works(dev, libmla)
+
+
+@pytest.mark.parametrize("call", ["decode", "combine", "get_error", "topk"])
+def test_refused_decode_calls_are_not_reported_again(dev, libmla, call):
+    from mla_latent_kv_26_b200.decoder import decoder_for
+    from mla_latent_kv_26_b200.workloads import small
+
+    d = small(batch=1, heads=2, lens=[70], seed=1)
+    dec = decoder_for(d, device=dev)
+    q, cache, bt, lens = (d[k].to(dev) for k in ("q", "cache", "block_table", "seq_lens"))
+    dec(q, cache, bt, lens)
+    x = torch.zeros(64, dtype=torch.int32, device=dev)
+    libmla.check(libmla.mla_topk(libmla.make_topk_desc(rows=1, num_keys=8, k=4), x, None, x[32:]), "mla_topk")
+    torch.cuda.synchronize(dev)
+    _merge_works(dev, libmla)
+    with _RefusingStream() as s:
+        if call == "topk":
+            st = libmla.mla_topk(libmla.make_topk_desc(rows=1, num_keys=8, k=4), x, None, x[32:], s)
+        elif call == "get_error":
+            st = libmla.mla_get_error(dec.plan, s)[0]
+        else:
+            with pytest.raises(libmla.MlaError) as e:
+                if call == "decode":
+                    dec.decode_step(q, cache, bt, lens, stream=s)
+                else:
+                    dec.combine_step(s)
+            st = e.value.status
+    assert st == libmla.MLA_ERR_CUDA
+    _merge_works(dev, libmla)
+    dec(q, cache, bt, lens)
+    assert dec.error()[0] == libmla.MLA_OK
