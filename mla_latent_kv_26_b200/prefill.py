@@ -8,10 +8,11 @@ latent cache, in three library calls (``include/mla_prefill.h``).
 
 The wrappers check dtypes, shapes and devices and pass raw pointers; all
 arithmetic happens in libmla's kernels. Offsets and lengths stay on the
-device, nothing synchronises, and a captured CUDA graph replays with other
+device, no call synchronises, and a captured CUDA graph replays with other
 lengths within the same capacities. ``stream`` (a torch stream or a raw handle;
 the current one when not given) is where a call's kernels run and where what it
-allocates belongs; inputs made on another stream are the caller's to order.
+allocates belongs; inputs made on another stream are the caller's to order and
+to keep.
 
 Sequence b's new tokens are rows ``[cu_q[b], cu_q[b + 1])`` of ``q`` and its
 keys rows ``[cu_k[b], cu_k[b + 1])`` of ``kv``: all its tokens, the new ones
@@ -249,9 +250,17 @@ def merge_parts(part_out: torch.Tensor, part_lse: torch.Tensor, *, stream=None) 
 class MlaPrefill:
     """The prefill of ragged chunks over the paged cache: read back, expand,
     attend. Keys and values are rounded to bf16 in between (2^-8 of each value at
-    most), as a bf16 kv up-projection of the model makes them. Owns the buffers for up to ``max_queries`` new tokens and
-    ``max_keys`` cached tokens (all sequences of a call together; 512 * H + 1152
-    bytes per key); a call with more is clipped and sets a bit of ``error_word``."""
+    most), as a bf16 kv up-projection of the model makes them. Owns the buffers for
+    up to ``max_queries`` new tokens and ``max_keys`` cached tokens (all sequences
+    of a call together; 512 * H + 1152 bytes per key); a call with more is clipped
+    and sets a bit of ``error_word``.
+
+    Calls of one object share its buffers and must not overlap: order them, also
+    across streams, or use an object for each. The constructor waits for the work
+    that its stream holds (unless that is being captured), so that the first call
+    may come on any stream. Buffers stay allocated for calls on a ``torch.cuda.Stream``
+    given as ``stream`` when the object goes away; it has to outlive calls on a
+    raw handle or an external stream, and graphs captured from it."""
 
     def __init__(self, *, max_queries: int, max_keys: int, num_heads: int,
                  softmax_scale: float = B.DEFAULT_SOFTMAX_SCALE, num_sms: int = 0, device="cuda"):
@@ -263,12 +272,25 @@ class MlaPrefill:
         with torch.cuda.device(dev):
             n = attention_workspace_bytes(max_queries, num_heads, max_keys, num_sms=num_sms)
         self.workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-        self.rows = torch.zeros(max_keys, 576, dtype=torch.bfloat16, device=dev)
+        self.rows = torch.empty(max_keys, 576, dtype=torch.bfloat16, device=dev)
         self.kv = torch.empty(max_keys, num_heads, 256, dtype=torch.bfloat16, device=dev)
         self.out = torch.empty(max_queries, num_heads, 128, dtype=torch.bfloat16, device=dev)
         self.lse = torch.empty(max_queries, num_heads, dtype=torch.float32, device=dev)
         self.error_word = torch.zeros(1, dtype=torch.int32, device=dev)
         self._expand_desc = B.make_expand_desc(num_rows=max_keys, num_heads=num_heads)
+        self._streams = set()  # handles of the streams that the buffers are recorded on
+        # the fill above, and whatever used this memory before, lie on this stream
+        with torch.cuda.device(dev):
+            if not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream(dev).synchronize()
+
+    def _record(self, stream):
+        """Ties the buffers to a stream that the allocator may still ask for its
+        work when they go away; not to an external one, which may be gone by then."""
+        if isinstance(stream, torch.cuda.Stream) and not isinstance(stream, torch.cuda.ExternalStream):
+            for t in (self.workspace, self.rows, self.kv, self.out, self.lse, self.error_word):
+                t.record_stream(stream)
+            self._streams.add(stream.cuda_stream)
 
     def __call__(self, q: torch.Tensor, wkv_b: torch.Tensor, kv_cache: torch.Tensor, block_table: torch.Tensor,
                  cu_q: torch.Tensor, cu_k: torch.Tensor, *, starts: Optional[torch.Tensor] = None,
@@ -287,6 +309,8 @@ class MlaPrefill:
         fp8, batch = _check_cache(kv_cache, block_table, cu_k, starts, dev)
         _check("cu_q", cu_q, _I32, (batch + 1,), dev)
         out, e = self.out[:nq], self.error_word
+        if stream is not None and getattr(stream, "cuda_stream", stream) not in self._streams:
+            self._record(stream)
         with _on(dev):
             s = _stream(stream, dev)
             _launch_read(fp8, kv_cache, block_table, cu_k, starts, self.rows, e, s)
