@@ -24,6 +24,7 @@ a causal descriptor does less work.
 from __future__ import annotations
 
 import contextlib
+import math
 from typing import Optional, Tuple
 
 import torch
@@ -274,12 +275,12 @@ class MlaPrefill:
         self.workspace = torch.empty(n, dtype=torch.uint8, device=dev)
         self.rows = torch.empty(max_keys, 576, dtype=torch.bfloat16, device=dev)
         self.kv = torch.empty(max_keys, num_heads, 256, dtype=torch.bfloat16, device=dev)
-        self.out = torch.empty(max_queries, num_heads, 128, dtype=torch.bfloat16, device=dev)
-        self.lse = torch.empty(max_queries, num_heads, dtype=torch.float32, device=dev)
+        self.out = torch.zeros(max_queries, num_heads, 128, dtype=torch.bfloat16, device=dev)
+        self.lse = torch.full((max_queries, num_heads), -math.inf, dtype=torch.float32, device=dev)
         self.error_word = torch.zeros(1, dtype=torch.int32, device=dev)
         self._expand_desc = B.make_expand_desc(num_rows=max_keys, num_heads=num_heads)
         self._streams = set()  # handles of the streams that the buffers are recorded on
-        # the fill above, and whatever used this memory before, lie on this stream
+        # the fills above, and whatever used this memory before, lie on this stream
         with torch.cuda.device(dev):
             if not torch.cuda.is_current_stream_capturing():
                 torch.cuda.current_stream(dev).synchronize()
@@ -298,7 +299,10 @@ class MlaPrefill:
         """``q`` [Nq, H, 192], Nq at most ``max_queries``; sequence b attends to
         its cached positions ``starts[b] .. starts[b] + cu_k[b + 1] - cu_k[b] - 1``
         (``starts`` None: from 0). Returns ``out`` [Nq, H, 128], a view of a
-        buffer that the next call overwrites; its log-sum-exp is ``self.lse[:Nq]``."""
+        buffer that the next call overwrites; its log-sum-exp is ``self.lse[:Nq]``.
+        Rows outside ``[cu_q[0], cu_q[batch])`` belong to no sequence and keep what
+        an earlier call left there, 0 and -inf where none did: a program whose
+        lengths on the device cover fewer than Nq rows takes only those."""
         dev = self.device
         if not isinstance(q, torch.Tensor) or q.dim() != 3 or q.shape[0] > self.out.shape[0]:
             raise ValueError(f"q: need a [queries, {self.num_heads}, 192] tensor of at most {self.out.shape[0]} queries")
