@@ -136,7 +136,8 @@ mla_status_t cache_read(const mlap_read_desc_t* d, const void* cache, const int3
                         cudaStream_t stream) {
   if (!d) return MLA_ERR_INVALID_ARG;
   if (d->batch < 0 || d->max_pages_per_seq < 1 || d->num_pages < 1 || d->num_rows < 0) return MLA_ERR_INVALID_ARG;
-  if (d->d_latent != kDLatent || d->d_rope != kDRope || d->page_size != kPage) return MLA_ERR_UNSUPPORTED;
+  if (d->d_latent != kDLatent || d->d_rope != kDRope || d->page_size != kPage || d->batch > kMaxBatch)
+    return MLA_ERR_UNSUPPORTED;
   if ((long long)d->num_pages * kPage > 0x7fffffffLL || (long long)d->max_pages_per_seq * kPage > 0x7fffffffLL ||
       d->num_rows > 0x7fffffff - kRowsPerWarp * kReadWarps)
     return MLA_ERR_UNSUPPORTED;

@@ -977,7 +977,7 @@ mla_status_t check_attention(const mlap_attention_desc_t* d) {
   if (d->batch < 0 || d->num_heads < 1 || d->num_q < 0 || d->num_k < 0 || (d->causal != 0 && d->causal != 1) ||
       d->num_sms < 0 || d->pe_stride < kDRope || !(d->softmax_scale > 0.f) || !isfinite(d->softmax_scale))
     return MLA_ERR_INVALID_ARG;
-  if (d->num_heads > kMaxHeads || d->d_nope != 128 || d->d_rope != kDRope || d->d_v != 128 || d->pe_stride % 8 != 0)
+  if (d->num_heads > kMaxHeads || d->batch > kMaxBatch || d->d_nope != 128 || d->d_rope != kDRope || d->d_v != 128 || d->pe_stride % 8 != 0)
     return MLA_ERR_UNSUPPORTED;
   // row indexes and tile counts are 32-bit
   if (d->num_q > 0x7fffffff - kBlockQ || d->num_k > 0x7fffffff - kTile) return MLA_ERR_UNSUPPORTED;

@@ -97,8 +97,8 @@ def _check_cache(kv_cache, block_table, row_offsets, starts, dev):
         raise ValueError("kv_cache must be [pages, 64, 576] bf16 or [pages, 64, 656] uint8, "
                          "block_table [batch, max_pages_per_seq]")
     batch, width = block_table.shape
-    if kv_cache.shape[0] == 0 or not 0 < width <= _INT_MAX:
-        raise ValueError("kv_cache, block_table: empty, or more than 2^31 - 1 pages per sequence")
+    if kv_cache.shape[0] == 0 or not 0 < width <= _INT_MAX or batch > _INT_MAX:
+        raise ValueError("kv_cache, block_table: empty, or more than 2^31 - 1 pages per sequence or sequences")
     _check("kv_cache", kv_cache, _U8 if fp8 else _BF16, None, dev)
     _check("block_table", block_table, _I32, None, dev)
     _check("row_offsets", row_offsets, _I32, (batch + 1,), dev)
@@ -208,8 +208,8 @@ def prefill_attention(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, cu_
     if k_pe.shape[0] != Nk:
         raise ValueError(f"k_pe: {k_pe.shape[0]} rows, kv has {Nk}")
     _check("cu_q", cu_q, _I32, None, dev)
-    if cu_q.dim() != 1 or cu_q.shape[0] < 1:
-        raise ValueError("cu_q: need batch + 1 offsets")
+    if cu_q.dim() != 1 or not 1 <= cu_q.shape[0] <= _INT_MAX:
+        raise ValueError("cu_q: need batch + 1 offsets, batch below 2^31")
     _check("cu_k", cu_k, _I32, cu_q.shape, dev)
     _optional_i32("error_word", error_word, dev)
     if out is None:
