@@ -8,9 +8,12 @@
  * run standard attention over them, 2 * (192 + 128) operations per query, head
  * and key, plus 2 * 512 * 256 per key and head for the expansion ("深度解读
  * DeepSeek：源码解读 DeepSeek-V3", section "MLA", the unabsorbed branch;
- * "DeepSeek-V2-Lite 模型结构详解", section "五、MLA：注意力"). The two are equal
- * at about 170 new tokens per sequence; below that mla_decode is the better
- * call. The three steps, in order, on one stream:
+ * "DeepSeek-V2-Lite 模型结构详解", section "五、MLA：注意力"). As operations the
+ * two are equal at about 170 new tokens per sequence. Measured, the three calls
+ * below take less time than absorb, decode and un-absorb from about 10 new tokens
+ * per sequence on with 16 heads, and with 128 heads from about 50 (8 sequences of
+ * 600 tokens), 90 (one of 4096 or 16384) or 130 (4 of 8192). In order, on one
+ * stream:
  *
  *   mlap_cache_read  -> rows of the sequences, read back from the paged cache
  *   mlap_expand_kv   -> per-head keys and values of those rows
