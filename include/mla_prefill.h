@@ -144,7 +144,7 @@ typedef struct {
   int32_t pe_stride;   /* elements between rows of k_pe, >= 64, a multiple of 8 */
   int32_t causal;      /* 0 or 1 */
   float softmax_scale; /* > 0; 1/sqrt(192) for DeepSeek V2/V3 */
-  int32_t num_sms;     /* SMs to spread the work over; 0 = all SMs of the current device */
+  int32_t num_sms;     /* SMs to spread the work over, in pairs (1: one pair); 0 = all of the current device */
   int32_t d_nope;      /* must be 128 */
   int32_t d_rope;      /* must be 64 */
   int32_t d_v;         /* must be 128 */

@@ -10,9 +10,10 @@
 // one tile is written while the next is computed). Tiles are dealt to the pairs
 // in runs, heads fastest, and a CTA's latents (128 KB for the whole K) stay in
 // shared memory for a run of heads: per 4096 cycles of products an SM loads
-// 128 KB of weights and nothing else. 8209 rows x 128 heads: 250 to 258 us,
-// 1.08 PFLOP/s, 0.9 of a library product of the size. (Loading both operands for
-// every tile of 128 x 256 on single CTAs, 384 KB per 4096 cycles, took 292 us.)
+// 128 KB of weights and nothing else. 8209 rows x 128 heads, replayed: 227 us,
+// 1.22 PFLOP/s in bursts at 1965 MHz, 257 us at 1.44 GHz under the power cap; a
+// library product of the size 238 and 276. (Loading both operands for every tile of
+// 128 x 256 on single CTAs, 384 KB per 4096 cycles, took 292 us when this took 280.)
 //
 // Per row and head 262144 operations and 512 bytes written: compute bound for
 // all but a few rows.

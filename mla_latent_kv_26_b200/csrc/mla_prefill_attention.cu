@@ -20,20 +20,32 @@
 // is (sequence, group of heads, block, head of the group, tile), with groups of
 // about as many heads as a run has items: pairs then work on the different
 // blocks of one sequence with the same heads, and so the same keys, at about the
-// same time, and share them in L2 (128 heads, 2048 queries over 16384 keys: 2.27
-// ms, 2.50 with all heads in one group). An item cut by a run boundary leaves
-// float32 partials with their own lse, merged by the second kernel.
-// Where keys and values are more than L2 keeps, whole items are dealt in rounds
-// before the runs (rounds_of), which keeps the pairs in step: the same call reads
-// 1.8 GB from HBM instead of 5.9, for 1.2 GB of inputs, and takes 2.14 ms instead
-// of 2.35; 16 heads, 16384 new tokens: 0.97 ms instead of 1.12. With two or three
-// blocks the keys are read too few times for that to pay: 600 queries over 7000
-// keys, 128 heads, 371 us in rounds, 357 in runs; with four (1024 over 8192)
-// within 1 % not causal, 484 us instead of 501 causal. Below 64 MiB of keys and
-// values rounds cost 2 to 3 % (4096 new tokens, 16 heads: 85 us for 83), from
-// there on they gain (2048, 64 heads: 94 us for 96). (A kernel that knows
-// rounds, on calls whose sequences have none: 400 prompts of 300 tokens 1.013 ms
-// instead of 0.993; calls too small for any get the one that does not.)
+// same time, and share them in L2 (128 heads, 2048 queries over 16384 keys, without
+// the rounds below: 2.05 ms, 2.14 with all heads in one group). An item cut by a run
+// boundary leaves float32 partials with their own lse, merged by the second kernel.
+// Where keys and values are many, whole items are dealt in rounds before the runs
+// (rounds_of), which keeps the pairs in step: the same call reads 1.8 GB from HBM
+// instead of 5.9, for 1.2 GB of inputs, and takes 1.89 ms instead of 2.05; 16
+// heads, 16384 new tokens: 0.99 ms instead of 1.08; 32 heads, 2048 queries over
+// 8192 keys: 239 us instead of 257. (Times of this comment, unless it says more:
+// replayed graphs in bursts of 20 ms, at 1965 MHz. Under the power cap, 2 s of
+// replays, these three take 2.17 for 2.42 ms, 1.13 for 1.25 ms, 275 for 301 us.)
+//
+// Where rounds begin, measured on both sides, causal unless said otherwise:
+// - 64 MiB of keys and values. Below: 32 MiB (4096 new tokens, 16 heads) 86.9 us in
+//   rounds, 85.0 in runs; 55 MiB (2048 over 3500, 32 heads) 101.9 and 102.1. Eight
+//   calls at 64 MiB, 16 to 128 heads: 0.1 to 2.5 % less time in rounds (4096, 32
+//   heads 156.8 for 160.8 us; 8192, 16 heads 274.0 for 280.6; 1024 over 2048, 64
+//   heads 73.2 for 73.3), four from 70 to 128 MiB 1 to 5 % less. A measured size, not
+//   L2's (126 MB).
+// - four blocks. 1024 queries over 8192 keys, 128 heads: 508 us for 512, not causal
+//   530 for 532. Two or three blocks go either way: 512 over 1024, 128 heads, 52.9
+//   us in rounds for 51.6 in runs, 300 over 2000 81.6 for 80.0, four sequences of
+//   512 over 4096 565 for 556; but 600 over 7000 335 for 337, 512 over 8192 285 for
+//   296. They stay in runs.
+// The host picks the kernel that knows rounds by num_q and num_k, which may be a
+// capacity; on many short sequences, which have none, it costs 3 % (400 prompts of
+// 300 tokens, 16 heads, 915 us for 888), from 1000 keys a sequence on nothing.
 //
 // A CTA pair (cta_group::2) works on a block: S = Q K^T and O += P V with M 256,
 // 128 rows in each CTA. Each CTA loads half of every key tile (64 keys of K,
@@ -64,8 +76,17 @@
 // Bound by the tensor cores and the softmax behind them: 1280 cycles of products
 // a tile, about 1650 taken (a warpgroup needs 2900 for its tile, 1024 of them
 // exponentials, every second tile is its). 2048 queries over 16384 keys, 128
-// heads, causal: 2.17 ms, 1.19 PFLOP/s at 1.2 to 1.3 GHz under the power cap;
-// 2048 over 8192 keys, 32 heads: 242 us, 1.24 PFLOP/s, tensor pipe 71 % active.
+// heads, causal: 1.89 ms, 1.36 PFLOP/s; 2.17 ms, 1.19 PFLOP/s at 1.40 GHz under
+// the power cap. 2048 over 8192 keys, 32 heads: 239 us, 1.26 PFLOP/s, tensor pipe
+// 71 % active.
+//
+// Roundings: scores, maxima, sums, O and split partials are float32. P is rounded
+// to bf16 because the tensor cores take both factors of P V in one type and V is
+// bf16; l sums the unrounded p. Random in sign, that adds to the rounding of out
+// an error of its size (2-norm relative to float64 0.0023; 0.0016 in float32
+// throughout with out rounded once).
+// Two ideas are published ones: rescaling O only when the maximum has grown by
+// more than a bound, and two softmax warpgroups on alternate tiles.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
@@ -95,8 +116,8 @@ constexpr int kAttnSmem = 1024 + 2 * kQBytes + kStages * kStageBytes;
 constexpr uint32_t kTmemO = 0, kTmemP = 128, kTmemS = 256, kTmemAll = 512;
 constexpr float kGrowth = 8.0f;            // log2: O is rescaled when a row's maximum grew by more (p stays below 2^8)
 constexpr int kItems = 8;                  // items handed on and not yet finished by every warp
-constexpr long long kShareBytes = 64ll << 20;  // keys and values that would not stay in L2 (126 MB)
-constexpr int kShareBlocks = 4;            // and that are read by so many blocks
+constexpr long long kShareBytes = 64ll << 20;  // keys and values of a sequence from which rounds pay (see above)
+constexpr int kShareBlocks = 4;            // and the blocks that read them
 constexpr int kKeyBytes = 512;             // of a head's key and value
 constexpr int kItemUnits = 3;              // cost of an item beside its tiles, in tiles
 // Registers a thread after the split: the softmax warpgroups hold a row of
@@ -165,7 +186,7 @@ struct Seq {
   }
 };
 
-// A sequence whose keys and values do not stay in L2 (kShareBytes) goes to the
+// A sequence with many keys and values (kShareBytes, kShareBlocks) goes to the
 // workers in rounds first, as long as there are items for all of them: heads
 // 2x and 2x + 1 give one turn for each block m, blocks m of the first and
 // blocks - 1 - m of the second, so that causal turns cost the same, and worker w

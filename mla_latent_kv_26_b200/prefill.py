@@ -255,7 +255,7 @@ class MlaPrefill:
     most), as a bf16 kv up-projection of the model makes them. Owns the buffers for
     up to ``max_queries`` new tokens and ``max_keys`` cached tokens (all sequences
     of a call together; 512 * H + 1152 bytes per key); a call with more is clipped
-    and sets a bit of ``error_word``.
+    and sets a bit of ``error_word``. ``num_sms`` bounds the attention's SMs alone.
 
     Calls of one object share its buffers and must not overlap: order them, also
     across streams, or use an object for each. The constructor waits for the work
