@@ -62,7 +62,7 @@ extern "C" {
  * zeros. row_offsets beyond num_rows or out of order set MLA_DEVERR_SEQ_LEN;
  * no row outside [0, num_rows) is touched. */
 typedef struct {
-  int32_t batch;             /* 0..2^24 */
+  int32_t batch;             /* 0..2^22 */
   int32_t max_pages_per_seq; /* block_table row stride (entries), >= 1 */
   int32_t num_pages;         /* physical pages in kv_cache, >= 1 */
   int32_t num_rows;          /* capacity of rows, >= 0 */
@@ -137,7 +137,7 @@ MLA_API mla_status_t mlap_expand_kv(const mlap_expand_desc_t* desc, const void* 
  * everything else is float32. The result does not depend on timing: work is
  * split by the lengths alone. */
 typedef struct {
-  int32_t batch;       /* 0..2^24 */
+  int32_t batch;       /* 0..2^22 */
   int32_t num_heads;   /* H: 1..128 */
   int32_t num_q;       /* rows of q, out, lse; >= 0 */
   int32_t num_k;       /* rows of kv and k_pe; >= 0 */

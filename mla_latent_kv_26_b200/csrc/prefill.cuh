@@ -13,10 +13,10 @@ namespace prefill {
 
 constexpr uint32_t kErrPosition = 0x10u;       // MLA_DEVERR_POSITION
 constexpr uint64_t kWaitNs = 2000000000ull;    // a pipeline wait gives up after 2 s: only a broken device gets there
-// Sequences of a call, as many as decode takes query tokens: indexes that step over
-// them stay in 32 bits, and a worker's search through the offsets of 2^24 sequences
-// takes 0.4 s, within the waits of the warps that it feeds.
-constexpr int kMaxBatch = 1 << 24;
+// Sequences of a call: indexes that step over them stay in 32 bits, and a worker
+// passes a run of empty ones within the waits of the warps that it feeds (84 ns
+// each: 2^20 between two sequences 88 ms, 2^22 0.35 s, 0.6 s at the lowest clocks).
+constexpr int kMaxBatch = 1 << 22;
 constexpr int kBox = 128 * 128;                // bytes of a 128-row x 64-column bf16 box (128-byte swizzle rows)
 
 MLA_DEV void set_error(uint32_t* word, uint32_t bits) {
