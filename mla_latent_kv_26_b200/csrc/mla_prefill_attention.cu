@@ -701,18 +701,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     // Their probabilities are 0, but 0 * NaN is NaN: whatever lies there is cleared.
     RingPos p;
     uint32_t phases = 0;  // of the entries of v_landed, which only some tiles use
+    int ahead = 0;        // tiles of the item before: this warp waits for an item's end, not tile by tile
 #pragma unroll 1
     for (int n = 0;; ++n) {
-      if (!W.wait_warp(&sh.item_full[n % kItems], (n / kItems) & 1)) break;
+      if (!W.wait_warp_tiles(&sh.item_full[n % kItems], (n / kItems) & 1, ahead)) break;
       const Item it = sh.item[n % kItems];
       const int t1 = it.t1;
       if (t1 == 0) break;
+      ahead = t1 - it.t0;
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&sh.item_free[n % kItems]));
 #pragma unroll 1
       for (int j = it.t0; j < t1 - 1; ++j) p.next();  // only an item's last tile can be its sequence's last
       if (tail(it, t1 - 1)) {
-        if (!W.wait_warp(&sh.v_landed[p.s], (phases >> p.s) & 1)) break;
+        if (!W.wait_warp_tiles(&sh.v_landed[p.s], (phases >> p.s) & 1, ahead)) break;
         phases ^= 1u << p.s;
         const uint32_t vs = stages + p.s * kStageBytes + kKBytes;
         for (int x = max(it.L - (t1 - 1) * kTile, 0) * 8 + lane; x < kTile * 8; x += 32)

@@ -13,6 +13,7 @@ namespace prefill {
 
 constexpr uint32_t kErrPosition = 0x10u;       // MLA_DEVERR_POSITION
 constexpr uint64_t kWaitNs = 2000000000ull;    // a pipeline wait gives up after 2 s: only a broken device gets there
+constexpr uint64_t kTileNs = 20000;            // more for a wait that lasts as long as a tile of 128 keys
 // Sequences of a call: indexes that step over them stay in 32 bits, and a worker
 // passes a run of empty ones within the waits of the warps that it feeds (84 ns
 // each: 2^20 between two sequences 88 ms, 2^22 0.35 s, 0.6 s at the lowest clocks).
@@ -35,7 +36,7 @@ struct Waiter {
     set_error(err, kErrTimeout);
   }
   template <bool kCluster>
-  MLA_DEV bool wait_impl(uint64_t* bar, uint32_t parity, bool drain) {
+  MLA_DEV bool wait_impl(uint64_t* bar, uint32_t parity, bool drain, uint64_t limit = kWaitNs) {
     const uint32_t a = smem_addr(bar);
     if (kCluster ? mbar_try_wait_cluster(a, parity) : mbar_try_wait(a, parity)) return true;
     const uint64_t t0 = global_timer_ns();
@@ -43,7 +44,7 @@ struct Waiter {
     while (true) {
       if (kCluster ? mbar_try_wait_cluster(a, parity) : mbar_try_wait(a, parity)) return true;
       if (!drain && aborted()) return false;
-      if (global_timer_ns() - t0 > kWaitNs) {
+      if (global_timer_ns() - t0 > limit) {
         fail();
         return false;
       }
@@ -57,6 +58,10 @@ struct Waiter {
   // Every lane waits; the outcome is made warp-uniform so that no lane leaves
   // a loop its warp-mates stay in.
   MLA_DEV bool wait_warp(uint64_t* bar, uint32_t parity) { return __all_sync(~0u, wait(bar, parity)); }
+  // As wait_warp, for what comes behind `tiles` key tiles of work at a microsecond or two each.
+  MLA_DEV bool wait_warp_tiles(uint64_t* bar, uint32_t parity, int tiles) {
+    return __all_sync(~0u, wait_impl<false>(bar, parity, false, kWaitNs + (uint64_t)tiles * kTileNs));
+  }
 };
 
 // a / b for a >= 0, b > 0: one 32-bit division where both fit, else bit by bit
