@@ -262,7 +262,8 @@ class MlaPrefill:
     that its stream holds (unless that is being captured), so that the first call
     may come on any stream. Buffers stay allocated for calls on a ``torch.cuda.Stream``
     given as ``stream`` when the object goes away; it has to outlive calls on a
-    raw handle or an external stream, and graphs captured from it."""
+    raw handle, an external stream or one that was only the current one, and graphs
+    captured from it."""
 
     def __init__(self, *, max_queries: int, max_keys: int, num_heads: int,
                  softmax_scale: float = B.DEFAULT_SOFTMAX_SCALE, num_sms: int = 0, device="cuda"):
